@@ -234,6 +234,93 @@ int muon_step_schedule(muon_handle* h, float* const* params,
                        int nesterov, float wd, int ns_steps,
                        const float* coeff_table, int table_rows, void* stream);
 
+/* muon_step_schedule with every gradient multiplied by *grad_scale (device
+ * float, read by the first kernel; NULL = 1) before it enters the momentum:
+ * the multiplier that muon_grad_norm leaves in out[1] clips the step without
+ * a pass over the gradients of its own. coeff_table NULL = the default triple
+ * (table_rows is then ignored). With grad_scale NULL, or a multiplier of 1,
+ * results are those of muon_step_schedule. */
+int muon_step_scaled(muon_handle* h, float* const* params,
+                     const void* const* grads, float* const* momenta,
+                     const int32_t* shapes, int count, float lr, float beta,
+                     int nesterov, float wd, int ns_steps,
+                     const float* coeff_table, int table_rows,
+                     const float* grad_scale, void* stream);
+
+/* ---- Gradients of the whole model, and the tensors Muon does not take ----
+ *
+ * Muon updates the 2D hidden matrices; embeddings, heads, norms and biases
+ * go to AdamW ("Why Muon Works", "2D hidden -> Muon, the rest -> AdamW"),
+ * and clipping looks at all of them together ("Por que AdamW ...", gradient
+ * clipping). The calls below take lists of tensors of any shape: tensor i is
+ * numels[i] (>= 0) consecutive elements of type dtypes[i], aligned to its
+ * element size; 2^40 elements at most in all. count may be 0. The arrays are
+ * host arrays, read during the call only. Nothing is allocated, uploaded or
+ * kept between calls: the pointer tables travel as kernel arguments and all
+ * scratch is the caller's, so calls on several streams are independent and
+ * every call may be captured in a CUDA graph. Sums are added in a fixed
+ * order: results repeat bit for bit. */
+
+/* Element types. */
+enum muon_dtype { MUON_DTYPE_F32 = 0, MUON_DTYPE_BF16 = 1, MUON_DTYPE_F16 = 2 };
+
+/* Norms of a list. */
+enum muon_norm_kind {
+  MUON_NORM_L2 = 0, /* sqrt of the sum of squares (added in fp64)           */
+  MUON_NORM_INF = 1 /* largest magnitude                                    */
+};
+
+/* Bytes of device scratch for a list of `count` tensors. */
+#define MUON_GRAD_SCRATCH_BYTES(count) ((size_t)8 * ((size_t)32768 + (size_t)(count)))
+
+/* Norm of all tensors together and its clip multiplier.
+ *   tensors    : device pointers; NULL skips tensor i (it adds nothing).
+ *   norm_kind  : enum muon_norm_kind.
+ *   max_norm   : >= 0; +infinity for no bound.
+ *   out        : device float[2]: the norm, and min(1, max_norm / (norm +
+ *                1e-6)); 1 without a bound. A NaN or infinite entry makes the
+ *                norm NaN or infinite, and the multiplier NaN or 0.
+ *   per_tensor : device float[count] or NULL: every tensor's norm (0 for a
+ *                skipped one).
+ *   scratch    : device memory, 8-byte aligned, scratch_bytes >=
+ *                MUON_GRAD_SCRATCH_BYTES(count); free for other use once the
+ *                stream has passed the call. */
+int muon_grad_norm(muon_handle* h, const void* const* tensors,
+                   const int64_t* numels, const int32_t* dtypes, int count,
+                   int norm_kind, float max_norm, float* out,
+                   float* per_tensor, void* scratch, size_t scratch_bytes,
+                   void* stream);
+
+/* Clipping: muon_grad_norm of src, then dst[i] = out[1] * src[i], rounded
+ * once to dst_dtypes[i]. dst[i] may be src[i] (same type: in place; not
+ * written when the multiplier is 1). Otherwise no written tensor may overlap
+ * another tensor of the call, nor may a tensor be listed twice. src[i] NULL
+ * skips tensor i. */
+int muon_clip_grads(muon_handle* h, const void* const* src, void* const* dst,
+                    const int64_t* numels, const int32_t* src_dtypes,
+                    const int32_t* dst_dtypes, int count, int norm_kind,
+                    float max_norm, float* out, void* scratch,
+                    size_t scratch_bytes, void* stream);
+
+/* One AdamW step, in place, on fp32 params and moments:
+ *   g = grad_scale * grad,  m' = beta1 m + (1 - beta1) g,
+ *   v' = beta2 v + (1 - beta2) g^2,
+ *   p' = p (1 - lr wd) - lr m'/(1 - beta1^t) / (sqrt(v'/(1 - beta2^t)) + eps).
+ *   grads      : NULL skips tensor i (nothing of it changes).
+ *   exp_avgs, exp_avg_sqs : m and v; zero before the first step.
+ *   step       : t, counted from 1; ignored when step_dev is given.
+ *   step_dev   : device int64 holding t, or NULL: a captured step reads the
+ *                number at every replay (the caller advances it).
+ *   grad_scale : device float or NULL (1): out + 1 of muon_grad_norm.
+ * No tensor may be listed twice or overlap another. */
+int muon_adamw_step(muon_handle* h, float* const* params,
+                    const void* const* grads, float* const* exp_avgs,
+                    float* const* exp_avg_sqs, const int64_t* numels,
+                    const int32_t* grad_dtypes, int count, double lr,
+                    double beta1, double beta2, double eps, double wd,
+                    int64_t step, const int64_t* step_dev,
+                    const float* grad_scale, void* stream);
+
 /* QK-Clip after a Muon step ("The Optimizer Wars", MuonClip): for every
  * weight i (fp32 W_q or W_k, device pointer, rows x cols, updated in place)
  * with shapes[i] = {rows, cols, head_rows} (rows a multiple of head_rows),
@@ -369,7 +456,11 @@ enum muon_kernel_kind {
   MUON_KERNEL_NS_FP32 = 6,       /* fp32 debug phase (one matrix)             */
   MUON_KERNEL_NS_SMALL = 7,      /* on-chip small-matrix path, all iterations */
   MUON_KERNEL_NORM_REDUCE = 8,   /* fixed-order norm sum (deterministic mode) */
-  MUON_KERNEL_NS_SYM = 9         /* symmetric-product phase of the Gram form  */
+  MUON_KERNEL_NS_SYM = 9,        /* symmetric-product phase of the Gram form  */
+  MUON_KERNEL_GRAD_NORM = 10,    /* partial norms of a list of gradients      */
+  MUON_KERNEL_GRAD_FINISH = 11,  /* their sum, the clip multiplier            */
+  MUON_KERNEL_GRAD_SCALE = 12,   /* clipped copy                              */
+  MUON_KERNEL_ADAMW = 13         /* AdamW update of a list of tensors         */
 };
 
 /* Per-launch timing for measurements. With max_calls > 0, each of the next

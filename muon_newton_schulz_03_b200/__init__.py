@@ -9,6 +9,13 @@ no Python or CPU fallback.
     opt = muon.Muon(device=0)                     # Moonlight scale, bf16 NS
     opt.step(params, grads, momenta, lr=2e-4)     # lists of 2D CUDA tensors
 
+A whole model's step, clipped: the norm is taken over every gradient, and the
+updates multiply by the clip factor as they read (no pass of its own):
+
+    norm, scale = opt.grad_norm(grads + other_grads, max_norm=1.0)
+    opt.step(params, grads, momenta, lr=2e-4, grad_scale=scale)
+    opt.adamw_step(others, other_grads, exp_avgs, exp_avg_sqs, lr=2e-4, step=t, grad_scale=scale)
+
 Readings of the method (see the C header): momentum EMA with the Nesterov
 blend, u / (||u||_F + 1e-7), five quintic Newton-Schulz steps with
 (3.4445, -4.7750, 2.0315) on the short side, scale * lr update with decoupled
@@ -19,6 +26,7 @@ lines").
 from __future__ import annotations
 
 import ctypes
+import math
 
 from ._lib import EXPORTED, MuonConfig, MuonError, check, lib_path, load
 
@@ -30,6 +38,8 @@ SCALE_MODES = {"moonlight": 0, "jordan": 1, "bernstein": 2, "none": 3}
 PRECISIONS = {"bf16": 0, "fp32": 1}
 ALGORITHMS = {"standard": 0, "gram": 1}
 FLAG_GRAD_BF16 = 1
+NORM_KINDS = {2: 0, math.inf: 1}
+GRAD_SCRATCH_DOUBLES = 32768    # MUON_GRAD_SCRATCH_BYTES(count) = 8 * (32768 + count)
 
 
 def round_up(x: int, k: int) -> int:
@@ -134,6 +144,97 @@ def _marshal_step(params, grads, momenta, host=False, device_index=None):
     n = len(pp)
     return ((ctypes.c_void_p * n)(*pp), (ctypes.c_void_p * n)(*gp), (ctypes.c_void_p * n)(*mp),
             (ctypes.c_int32 * (3 * n))(*flat), n)
+
+
+# -- lists of tensors of any shape ------------------------------------------
+
+_GRAD_DTYPES = None
+
+
+def _grad_dtypes():
+    global _GRAD_DTYPES
+    if _GRAD_DTYPES is None:
+        import torch
+        _GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    return _GRAD_DTYPES
+
+
+def _dense(t):
+    """Whether the elements of t fill one stretch of memory, in any order of dimensions."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+def _check_tensor(t, what, dtypes, device, like=None):
+    """A dense tensor of one of the types, on the CUDA device, laid out like another one."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a tensor, got {type(t).__name__}")
+    if t.layout != torch.strided:
+        raise ValueError(f"{what} must be a strided tensor, got {t.layout}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} must have dtype in {tuple(dtypes)}, got {t.dtype}")
+    if t.is_neg() or not _dense(t):
+        raise ValueError(f"{what} must be dense (its elements one stretch of memory), "
+                         f"got shape {tuple(t.shape)} with strides {t.stride()}")
+    if like is not None:
+        if t.shape != like.shape:
+            raise ValueError(f"{what} shape {tuple(t.shape)} != {tuple(like.shape)}")
+        if not (t.is_contiguous() and like.is_contiguous()) and t.stride() != like.stride():
+            raise ValueError(f"{what} has strides {t.stride()}, its partner {like.stride()}")
+    if t.device.type != "cuda" or t.device.index != device:
+        raise ValueError(f"{what} must be on cuda:{device}, got {t.device}")
+
+
+def _marshal_lists(device, dtypes, lists):
+    """Pointer arrays, element counts and types of paired tensor lists.
+
+    ``lists`` is [(name, tensors, allowed dtypes), ...]; where an entry of
+    the first is None, the entry is skipped (its partners are not looked at).
+    Returns ([pointer array per list], numels, [type array per list], count).
+    """
+    first = lists[0][1]
+    n = len(first)
+    for name, ts, _ in lists[1:]:
+        if len(ts) != n:
+            raise ValueError(f"{name} has {len(ts)} entries, {lists[0][0]} has {n}")
+    numels = (ctypes.c_int64 * n)()
+    ptrs = [(ctypes.c_void_p * n)() for _ in lists]
+    types = [(ctypes.c_int32 * n)() for _ in lists]
+    for i, t in enumerate(first):
+        if t is None:
+            continue
+        for (name, ts, allowed), pa, ta in zip(lists, ptrs, types):
+            x = ts[i]
+            _check_tensor(x, f"{name}[{i}]", allowed, device, None if x is t else t)
+            pa[i] = x.data_ptr()
+            ta[i] = dtypes[x.dtype]
+        numels[i] = t.numel()
+    return ptrs, numels, types, n
+
+
+def _check_scalar(t, what, dtype, device):
+    """A one-element CUDA tensor, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != 1:
+        raise ValueError(f"{what} must be a {dtype} tensor of one element")
+    if t.device.type != "cuda" or t.device.index != device:
+        raise ValueError(f"{what} must be on cuda:{device}, got {t.device}")
+    return t.data_ptr()
+
+
+def _norm_kind(norm_type):
+    kind = NORM_KINDS.get(norm_type)
+    if kind is None:
+        raise ValueError(f"norm_type must be 2 or inf, got {norm_type}")
+    return kind
 
 
 def x_layout(m: int, n: int, dtype, device):
@@ -283,7 +384,7 @@ class Muon:
 
     # -- full step ----------------------------------------------------------
     def step(self, params, grads, momenta, lr, beta=0.95, nesterov=True, wd=0.1, ns_steps=5, coeffs=None,
-             stream=None, row_splits=None):
+             stream=None, row_splits=None, grad_scale=None):
         """One Muon step, in place on params and momenta (lists of CUDA tensors).
 
         A ``None`` gradient skips its matrix. ``row_splits`` (optional, one
@@ -291,24 +392,112 @@ class Muon:
         an int h cuts it into row blocks of h rows, a list gives the block
         heights; every block is then a Muon matrix of its own (its rows are
         contiguous, so the blocks are passed as views, no copy).
+        ``grad_scale`` (a float32 CUDA tensor of one element, as ``grad_norm``
+        returns it) multiplies every gradient before it enters the momentum.
         """
         if row_splits is not None:
             params, grads, momenta = split_rows(params, grads, momenta, row_splits)
         pa, ga, ma, sa, n = _marshal_step(params, grads, momenta, device_index=self.device)
+        if grad_scale is not None:
+            import torch
+            check(self._lib.muon_step_scaled(self._h, pa, ga, ma, sa, n, float(lr), float(beta), int(bool(nesterov)),
+                                             float(wd), int(ns_steps), _coeffs(coeffs), 1,
+                                             _check_scalar(grad_scale, "grad_scale", torch.float32, self.device),
+                                             _stream_handle(stream)))
+            return
         check(self._lib.muon_step(self._h, pa, ga, ma, sa, n, float(lr), float(beta), int(bool(nesterov)),
                                   float(wd), int(ns_steps), _coeffs(coeffs), _stream_handle(stream)))
 
     def step_schedule(self, params, grads, momenta, coeff_table, lr, beta=0.95, nesterov=True, wd=0.1,
-                      stream=None):
-        """One Muon step whose Newton-Schulz iteration t uses coeff_table[t] = (a, b, c)."""
+                      stream=None, grad_scale=None):
+        """One Muon step whose Newton-Schulz iteration t uses coeff_table[t] = (a, b, c); ``grad_scale`` as in ``step``."""
         import torch
         rows = [tuple(float(v) for v in r) for r in coeff_table]
         if not rows or any(len(r) != 3 for r in rows):
             raise ValueError("coeff_table must be a non-empty list of (a, b, c)")
         table = (ctypes.c_float * (3 * len(rows)))(*[v for r in rows for v in r])
         pa, ga, ma, sa, n = _marshal_step(params, grads, momenta, device_index=self.device)
-        check(self._lib.muon_step_schedule(self._h, pa, ga, ma, sa, n, float(lr), float(beta), int(bool(nesterov)),
-                                           float(wd), len(rows), table, len(rows), _stream_handle(stream)))
+        check(self._lib.muon_step_scaled(self._h, pa, ga, ma, sa, n, float(lr), float(beta), int(bool(nesterov)),
+                                         float(wd), len(rows), table, len(rows),
+                                         _check_scalar(grad_scale, "grad_scale", torch.float32, self.device),
+                                         _stream_handle(stream)))
+
+    # -- gradients of the whole model, and the tensors Muon does not take ----
+    def _stream_of(self, stream):
+        """The torch stream of a call: the one given, else the current one of the handle's device."""
+        import torch
+        return torch.cuda.current_stream(self.device) if stream is None else stream
+
+    def _grad_buffers(self, count, per_tensor, stream):
+        """Results and scratch of a norm, from the call's stream's memory."""
+        import torch
+        with torch.cuda.stream(stream):
+            out = torch.empty(2, dtype=torch.float32, device=f"cuda:{self.device}")
+            per = torch.empty(count, dtype=torch.float32, device=out.device) if per_tensor else None
+            scratch = torch.empty(GRAD_SCRATCH_DOUBLES + count, dtype=torch.float64, device=out.device)
+        return out, per, scratch
+
+    def grad_norm(self, tensors, max_norm=None, norm_type=2.0, per_tensor=False, stream=None):
+        """Norm of all the tensors together and its clip multiplier, on the device.
+
+        ``tensors``: fp32, bf16 or fp16 CUDA tensors of any shape, dense; a
+        ``None`` adds nothing. ``norm_type``: 2 or inf. Returns (norm, scale),
+        two float32 CUDA scalars with scale = min(1, max_norm / (norm + 1e-6))
+        (1 without a ``max_norm``), and with ``per_tensor`` a third, the
+        norm of each tensor (0 for a ``None``). Nothing waits for the GPU;
+        pass ``scale`` on as ``grad_scale``. A NaN or infinity among the
+        entries makes the norm NaN or infinite, the multiplier NaN or 0.
+        """
+        kind = _norm_kind(norm_type)
+        types = _grad_dtypes()
+        (pa,), na, (ta,), n = _marshal_lists(self.device, types, [("tensors", list(tensors), types)])
+        st = self._stream_of(stream)
+        out, per, scratch = self._grad_buffers(n, per_tensor, st)
+        check(self._lib.muon_grad_norm(self._h, pa, na, ta, n, kind, math.inf if max_norm is None else float(max_norm),
+                                       out.data_ptr(), _ptr(per), scratch.data_ptr(), 8 * scratch.numel(),
+                                       _stream_handle(st)))
+        return (out[0], out[1], per) if per_tensor else (out[0], out[1])
+
+    def clip_grads(self, grads, max_norm, norm_type=2.0, out=None, stream=None):
+        """Multiply the gradients by min(1, max_norm / (norm + 1e-6)); returns the norm before (float32 CUDA scalar).
+
+        In place, or into the tensors of ``out`` (same shapes and strides,
+        fp32, bf16 or fp16). ``grads`` as in ``grad_norm``; no tensor twice.
+        """
+        kind = _norm_kind(norm_type)
+        types = _grad_dtypes()
+        grads = list(grads)
+        (sa, da), na, (st_, dt), n = _marshal_lists(
+            self.device, types, [("grads", grads, types), ("out", grads if out is None else list(out), types)])
+        st = self._stream_of(stream)
+        res, _, scratch = self._grad_buffers(n, False, st)
+        check(self._lib.muon_clip_grads(self._h, sa, da, na, st_, dt, n, kind, float(max_norm), res.data_ptr(),
+                                        scratch.data_ptr(), 8 * scratch.numel(), _stream_handle(st)))
+        return res[0]
+
+    def adamw_step(self, params, grads, exp_avgs, exp_avg_sqs, lr, step, betas=(0.9, 0.999), eps=1e-8, wd=0.1,
+                   grad_scale=None, stream=None):
+        """One AdamW step, in place on params, exp_avgs and exp_avg_sqs.
+
+        For the tensors Muon does not take (embeddings, heads, norms, biases):
+        fp32 CUDA tensors of any shape; grads fp32, bf16 or fp16, ``None``
+        skips. The tensors of one entry have one shape and one dense layout.
+        ``step`` counts from 1: an int, or an int64 CUDA tensor of one element
+        that a captured step reads at every replay (the caller advances it).
+        ``grad_scale``: as in ``step``.
+        """
+        import torch
+        types = _grad_dtypes()
+        f32 = (torch.float32,)
+        (ga, pa, ma, va), na, (ta, *_), n = _marshal_lists(
+            self.device, types, [("grads", list(grads), types), ("params", list(params), f32),
+                                 ("exp_avgs", list(exp_avgs), f32), ("exp_avg_sqs", list(exp_avg_sqs), f32)])
+        on_device = isinstance(step, torch.Tensor)
+        check(self._lib.muon_adamw_step(
+            self._h, pa, ga, ma, va, na, ta, n, float(lr), float(betas[0]), float(betas[1]), float(eps), float(wd),
+            0 if on_device else int(step), _check_scalar(step, "step", torch.int64, self.device) if on_device else None,
+            _check_scalar(grad_scale, "grad_scale", torch.float32, self.device),
+            _stream_handle(self._stream_of(stream))))
 
     def qk_clip(self, weights, s_max, head_rows, tau=100.0, stream=None):
         """QK-Clip in place on W_q / W_k weights (fp32 CUDA tensors).
@@ -425,7 +614,7 @@ class Muon:
         return base.value or 0, size.value
 
     KERNEL_KINDS = ("momentum_norm", "ns_gram", "ns_poly", "ns_comb", "apply", "scale_copy", "ns_fp32", "ns_small",
-                    "norm_reduce", "ns_sym")
+                    "norm_reduce", "ns_sym", "grad_norm", "grad_finish", "grad_scale", "adamw")
 
     def profile_enable(self, max_calls: int):
         """Record CUDA events around every kernel of the next max_calls calls."""

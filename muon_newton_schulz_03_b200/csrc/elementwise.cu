@@ -98,8 +98,11 @@ __device__ __forceinline__ unsigned block_count(unsigned v, unsigned* red) {
   return t;
 }
 
-// Momentum, Nesterov blend and u for one element (fp32, the lerp forms).
-__device__ __forceinline__ float momentum_u(float g, float& m, float beta, float one_minus_beta, int nesterov) {
+// Momentum, Nesterov blend and u for one element (fp32, the lerp forms), of
+// the gradient times gs (1 leaves it as it is, NaN and infinities too).
+__device__ __forceinline__ float momentum_u(float g, float& m, float beta, float one_minus_beta, int nesterov,
+                                            float gs) {
+  g = __fmul_rn(g, gs);
   const float mn = fmaf(beta, m, one_minus_beta * g);   // beta*m + (1-beta)*g
   m = mn;
   return nesterov ? fmaf(beta, mn - g, g) : mn;          // g + beta*(m' - g)
@@ -109,7 +112,7 @@ template <bool kFp32Out>
 __global__ void __launch_bounds__(kThreads) k1_momentum_norm(
     const MatPlan* __restrict__ plans, const MatBind* __restrict__ binds, const long long* __restrict__ prefix,
     int count, long long block_base, int ysel, float beta, int nesterov, double* __restrict__ sumsq,
-    double* __restrict__ partials, DevStatus* status, int check_nonfinite) {
+    double* __restrict__ partials, DevStatus* status, int check_nonfinite, const float* __restrict__ grad_scale) {
   __shared__ double red[kThreads / 32];
   __shared__ unsigned redc[kThreads / 32];
   const long long blk = (long long)blockIdx.x + block_base;
@@ -120,6 +123,7 @@ __global__ void __launch_bounds__(kThreads) k1_momentum_norm(
   const long long e0 = (blk - prefix[mat]) * (long long)kElemChunk;
   const long long e1 = min(e0 + (long long)kElemChunk, mp.numel);
   const float omb = 1.0f - beta;
+  const float gs = grad_scale != nullptr ? __ldg(grad_scale) : 1.0f;
   void* ybase = const_cast<void*>(sel_buf(mp, mb, ysel));
   const bool g_bf16 = (mb.flags & 1) != 0;
 
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) k1_momentum_norm(
       float u[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        u[i] = momentum_u(g[b][i], m[b][i], beta, omb, nesterov);
+        u[i] = momentum_u(g[b][i], m[b][i], beta, omb, nesterov, gs);
         acc += (double)u[i] * (double)u[i];
         if (check_nonfinite) bad += !isfinite(u[i]);
       }
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) k1_momentum_norm(
       load8_f32(mb.mom + e, m);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        u[i] = momentum_u(g[i], m[i], beta, omb, nesterov);
+        u[i] = momentum_u(g[i], m[i], beta, omb, nesterov, gs);
         acc += (double)u[i] * (double)u[i];
         if (check_nonfinite) bad += !isfinite(u[i]);
       }
@@ -177,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) k1_momentum_norm(
       const float g = g_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(mb.g)[e])
                              : static_cast<const float*>(mb.g)[e];
       float m = mb.mom[e];
-      const float u = momentum_u(g, m, beta, omb, nesterov);
+      const float u = momentum_u(g, m, beta, omb, nesterov, gs);
       mb.mom[e] = m;
       acc += (double)u * (double)u;
       if (check_nonfinite) bad += !isfinite(u);
@@ -332,16 +336,16 @@ cudaError_t launch_qk_clip(float* w, long long rows, long long cols, int head_ro
 
 cudaError_t launch_momentum_norm(const ElemLaunch& L, int ysel, float beta, int nesterov, double* sumsq,
                                  double* partials, DevStatus* status, int check_nonfinite, bool fp32_out,
-                                 cudaStream_t st) {
+                                 const float* grad_scale, cudaStream_t st) {
   if (L.nblocks <= 0) return cudaSuccess;
   if (fp32_out)
     k1_momentum_norm<true><<<(unsigned)L.nblocks, kThreads, 0, st>>>(L.plans, L.binds, L.prefix, L.count,
                                                                       L.block_base, ysel, beta, nesterov, sumsq,
-                                                                      partials, status, check_nonfinite);
+                                                                      partials, status, check_nonfinite, grad_scale);
   else
     k1_momentum_norm<false><<<(unsigned)L.nblocks, kThreads, 0, st>>>(L.plans, L.binds, L.prefix, L.count,
                                                                        L.block_base, ysel, beta, nesterov, sumsq,
-                                                                       partials, status, check_nonfinite);
+                                                                       partials, status, check_nonfinite, grad_scale);
   return cudaGetLastError();
 }
 

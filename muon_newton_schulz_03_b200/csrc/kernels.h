@@ -22,9 +22,10 @@ struct ElemLaunch {
 // partials == nullptr: one double atomic per block into sumsq; else each
 // block stores its partial at partials[block] and launch_reduce_partials
 // adds them per matrix in a fixed order (bitwise reproducible norms).
+// grad_scale (device, or NULL = 1) multiplies every gradient as it is read.
 cudaError_t launch_momentum_norm(const ElemLaunch& L, int ysel, float beta, int nesterov, double* sumsq,
                                  double* partials, DevStatus* status, int check_nonfinite, bool fp32_out,
-                                 cudaStream_t st);
+                                 const float* grad_scale, cudaStream_t st);
 cudaError_t launch_reduce_partials(const ElemLaunch& L, int m0, int m1, const double* partials, double* sumsq,
                                    cudaStream_t st);
 cudaError_t launch_apply(const ElemLaunch& L, int osel, float lr, float wd, int scale_mode, float extra_scale,
@@ -152,6 +153,99 @@ cudaError_t launch_ns_phase_fp32(const MatPlan& mp_host, int mat, int phase, con
                                  const double* sumsq, int first, float a, float b, float c, cudaStream_t st);
 
 int ns_bf16_smem_bytes();
+
+// ---------------------------------------------------------------------------
+// Operators on lists of gradients (grad_ops.cu)
+// ---------------------------------------------------------------------------
+
+enum GradType : int { GRAD_F32 = 0, GRAD_BF16 = 1, GRAD_F16 = 2 };   // muon_dtype
+enum GradNorm : int { GRAD_NORM_L2 = 0, GRAD_NORM_INF = 1 };         // muon_norm_kind
+
+// One tensor of a list: numel = 0 for a skipped one.
+struct GradItem {
+  const void* src;
+  void* dst;          // clipped copy only
+  long long numel;
+  int stype, dtype;
+};
+struct AdamItem {
+  float* p;
+  const void* g;
+  float* m;
+  float* v;
+  long long numel;
+  int gtype;
+};
+
+// Tables that travel as kernel arguments (at most 32,764 bytes of them). A
+// launch takes the small table when the list fits, to copy less.
+constexpr int kGradCapSmall = 64;
+constexpr int kNormCap = 1536;    // 20 bytes a tensor
+constexpr int kScaleCap = 1088;   // 28
+constexpr int kAdamCap = 704;     // 44
+constexpr int kNoPhase = 15;
+constexpr int kGradUnits = 32768; // at most this many blocks, and one more per tensor, share a norm
+
+// numel (48 bits) | source type | destination type | phase
+__host__ __device__ inline unsigned long long grad_meta(long long numel, int stype, int dtype, int phase) {
+  return (unsigned long long)numel | ((unsigned long long)stype << 48) | ((unsigned long long)dtype << 50) |
+         ((unsigned long long)phase << 52);
+}
+__host__ __device__ inline long long grad_numel(unsigned long long m) { return (long long)(m & 0xffffffffffffull); }
+__host__ __device__ inline int grad_src(unsigned long long m) { return (int)(m >> 48) & 3; }
+__host__ __device__ inline int grad_dst(unsigned long long m) { return (int)(m >> 50) & 3; }
+__host__ __device__ inline int grad_phase(unsigned long long m) { return (int)(m >> 52) & 15; }
+__host__ __device__ inline int grad_units(long long numel, int unit) { return (int)((numel + unit - 1) / unit); }
+
+template <int kCap>
+struct GradTable {
+  const void* src[kCap];
+  unsigned long long meta[kCap];
+  int unit0[kCap + 1];
+  int count;
+};
+template <int kCap>
+struct ScaleTable {
+  const void* src[kCap];
+  void* dst[kCap];
+  unsigned long long meta[kCap];
+  int unit0[kCap + 1];
+  int count;
+};
+template <int kCap>
+struct AdamTable {
+  float* p[kCap];
+  const void* g[kCap];
+  float* m[kCap];
+  float* v[kCap];
+  unsigned long long meta[kCap];
+  int unit0[kCap + 1];
+  int count;
+};
+struct SpanTable {
+  int unit0[kNormCap + 1];
+  int count;
+};
+
+struct AdamArgs {
+  double lr, beta1, beta2;
+  float decay, eps;                 // 1 - lr wd
+  float step_size, rsqrt_bc2;       // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t); unused with `step`
+  const long long* step;            // device step number, or NULL
+  const float* grad_scale;          // device multiplier of the gradients, or NULL
+};
+
+// Each launches one kernel over up to the table's capacity of tensors.
+// Partial k of the launch is the norm of its unit k; `units` is their number.
+cudaError_t launch_grad_norm(const GradItem* it, int n, int unit, int units, int kind, double* partials,
+                             cudaStream_t st);
+// out (or NULL): norm and clip multiplier over all `nunits` partials at `all`.
+// per_tensor (or NULL): norms of these n tensors, whose partials start at `partials`.
+cudaError_t launch_grad_finish(const GradItem* it, int n, int unit, int kind, const double* all, long long nunits,
+                               float max_norm, float* out, const double* partials, float* per_tensor,
+                               cudaStream_t st);
+cudaError_t launch_grad_scale(const GradItem* it, int n, int unit, int units, const float* scale, cudaStream_t st);
+cudaError_t launch_adamw(const AdamItem* it, int n, int unit, int units, const AdamArgs& a, cudaStream_t st);
 
 // Sets the calling thread's muon_last_error text.
 void record_last_error(const std::string& msg);

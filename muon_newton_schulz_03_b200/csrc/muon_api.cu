@@ -1106,8 +1106,8 @@ int step_p_maps(muon_handle* h, float* const* params, const std::vector<MatBind>
 }
 
 int enqueue_step_range(muon_handle* h, const MatBind* db, const std::vector<MatBind>& hb, const WorkRange& R,
-                       float lr, float beta, int nesterov, float wd, int ns_steps, const float* abc, cudaStream_t st,
-                       int* launches, const TmapBlob* d_p_maps) {
+                       float lr, float beta, int nesterov, float wd, int ns_steps, const float* abc,
+                       const float* grad_scale, cudaStream_t st, int* launches, const TmapBlob* d_p_maps) {
   DevPlan& P = *h->plan;
   double* sumsq = static_cast<double*>(P.ws);
   const bool fp32 = h->cfg.ns_precision == MUON_NS_FP32;
@@ -1116,7 +1116,7 @@ int enqueue_step_range(muon_handle* h, const MatBind* db, const std::vector<MatB
   const ElemLaunch EL = elem_launch(P, db, R);
   int slot = prof_before(h, MUON_KERNEL_MOMENTUM_NORM, st);
   MUON_CUDA_TRY(launch_momentum_norm(EL, BUF_X0, beta, nesterov ? 1 : 0, sumsq, P.partials, h->status,
-                                     h->cfg.check_nonfinite, fp32, st));
+                                     h->cfg.check_nonfinite, fp32, grad_scale, st));
   prof_after(h, slot, st);
   ++*launches;
   if (P.partials) {
@@ -1148,7 +1148,7 @@ int enqueue_step_range(muon_handle* h, const MatBind* db, const std::vector<MatB
 
 int step_impl(muon_handle* h, float* const* params, const void* const* grads, float* const* momenta,
               const int32_t* shapes, int count, float lr, float beta, int nesterov, float wd, int ns_steps,
-              const float* abc, cudaStream_t st) {
+              const float* abc, const float* grad_scale, cudaStream_t st) {
   int rc;
   if ((rc = ensure_plan(h, shapes, count))) return rc;
   CallTables ct{h, st};
@@ -1164,10 +1164,126 @@ int step_impl(muon_handle* h, float* const* params, const void* const* grads, fl
   if ((rc = step_p_maps(h, params, hb, ns_steps, st, &d_p_maps))) return rc;
   // Groups under the workspace cap run one after another on the stream.
   for (const WorkRange& R : ranges)
-    if ((rc = enqueue_step_range(h, db, hb, R, lr, beta, nesterov, wd, ns_steps, abc, st, &launches, d_p_maps)))
+    if ((rc = enqueue_step_range(h, db, hb, R, lr, beta, nesterov, wd, ns_steps, abc, grad_scale, st,
+                                 &launches, d_p_maps)))
       return rc;
   (void)P;
   h->last_launches = launches;
+  return MUON_OK;
+}
+
+// ---- Operators on lists of gradients ----
+
+constexpr long long kGradMaxNumel = 1ll << 40;   // of one list
+
+int bad_tensor(const char* what, int i, const char* why) {
+  return fail(MUON_ERR_INVALID_ARG, std::string(what) + "[" + std::to_string(i) + "] " + why);
+}
+
+size_t dtype_size(int t) { return t == MUON_DTYPE_F32 ? 4 : 2; }
+
+int check_list(const int64_t* numels, const int32_t* dtypes, int count, const char* what, long long* total) {
+  if (count < 0) return fail(MUON_ERR_INVALID_ARG, "count must be >= 0");
+  if (count > 0 && (!numels || !dtypes)) return fail(MUON_ERR_INVALID_ARG, "numels and dtypes arrays are required");
+  *total = 0;
+  for (int i = 0; i < count; ++i) {
+    if (numels[i] < 0 || numels[i] > kGradMaxNumel) return bad_tensor(what, i, "has a bad number of elements");
+    if (dtypes[i] < MUON_DTYPE_F32 || dtypes[i] > MUON_DTYPE_F16) return bad_tensor(what, i, "has an unknown dtype");
+    *total += numels[i];
+    if (*total > kGradMaxNumel) return fail(MUON_ERR_INVALID_ARG, "the tensors hold more than 2^40 elements");
+  }
+  return MUON_OK;
+}
+
+int check_elem_ptr(const void* p, size_t esize, const char* what, int i) {
+  if (p == nullptr) return bad_tensor(what, i, "is NULL");
+  if (reinterpret_cast<uintptr_t>(p) % esize) return bad_tensor(what, i, "is not aligned to its element size");
+  return MUON_OK;
+}
+
+// Memory ranges of a call: no written one may meet any other.
+struct Ranges {
+  struct R { uintptr_t a, b; bool written; };
+  std::vector<R> r;
+  void add(const void* p, size_t bytes, bool written) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    if (bytes) r.push_back({a, a + bytes, written});
+  }
+  bool clash() {
+    std::sort(r.begin(), r.end(), [](const R& x, const R& y) { return x.a < y.a; });
+    uintptr_t any = 0, written = 0;
+    for (const R& x : r) {
+      if (x.a < written || (x.written && x.a < any)) return true;
+      any = std::max(any, x.b);
+      if (x.written) written = std::max(written, x.b);
+    }
+    return false;
+  }
+};
+
+// Elements a block takes: about `units` blocks for the list, at least `least`
+// elements each, a multiple of 2048 (256 threads x 8 elements).
+int pick_unit(long long total, long long units, long long least) {
+  const long long u = std::max(least, (total + units - 1) / units);
+  return (int)((u + 2047) / 2048 * 2048);
+}
+
+long long count_units(const std::vector<GradItem>& it, int unit) {
+  long long u = 0;
+  for (const GradItem& x : it) u += grad_units(x.numel, unit);
+  return u;
+}
+
+// Norm of the list into out (norm, multiplier) and per_tensor; the caller has
+// checked everything.
+int enqueue_grad_norm(muon_handle* h, const std::vector<GradItem>& it, long long total, int kind, float max_norm,
+                      float* out, float* per_tensor, double* partials, cudaStream_t st, int* launches) {
+  const int unit = pick_unit(total, kGradUnits, 8192);
+  const long long nunits = count_units(it, unit);
+  const int count = (int)it.size();
+  long long base = 0;
+  for (int i0 = 0; i0 < count; i0 += kNormCap) {
+    const int n = std::min(kNormCap, count - i0);
+    int units = 0;
+    for (int i = 0; i < n; ++i) units += grad_units(it[i0 + i].numel, unit);
+    if (units > 0) {
+      const int slot = prof_before(h, MUON_KERNEL_GRAD_NORM, st);
+      MUON_CUDA_TRY(launch_grad_norm(&it[i0], n, unit, units, kind, partials + base, st));
+      prof_after(h, slot, st);
+      ++*launches;
+    }
+    base += units;
+  }
+  base = 0;
+  int i0 = 0;
+  do {
+    const int n = std::min(kNormCap, count - i0);
+    const bool last = i0 + n >= count;
+    if (per_tensor || last) {
+      const int slot = prof_before(h, MUON_KERNEL_GRAD_FINISH, st);
+      MUON_CUDA_TRY(launch_grad_finish(it.data() + i0, n, unit, kind, partials, nunits, max_norm,
+                                       last ? out : nullptr, partials + base,
+                                       per_tensor ? per_tensor + i0 : nullptr, st));
+      prof_after(h, slot, st);
+      ++*launches;
+    }
+    for (int i = 0; i < n; ++i) base += grad_units(it[i0 + i].numel, unit);
+    i0 += n;
+  } while (i0 < count);
+  return MUON_OK;
+}
+
+int check_norm_args(int norm_kind, float max_norm, const float* out, const void* scratch, size_t scratch_bytes,
+                    int count) {
+  if (norm_kind != MUON_NORM_L2 && norm_kind != MUON_NORM_INF) return fail(MUON_ERR_INVALID_ARG, "unknown norm_kind");
+  if (!(max_norm >= 0.0f)) return fail(MUON_ERR_INVALID_ARG, "max_norm must be >= 0 (infinity: no bound)");
+  if (!out || reinterpret_cast<uintptr_t>(out) % 4) return fail(MUON_ERR_INVALID_ARG, "out is NULL or misaligned");
+  if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 8)
+    return fail(MUON_ERR_INVALID_ARG, "scratch is NULL or not 8-byte aligned");
+  const size_t need = MUON_GRAD_SCRATCH_BYTES(count);
+  if (scratch_bytes < need)
+    return fail(MUON_ERR_INVALID_ARG, "scratch holds " + std::to_string(scratch_bytes) + " bytes, " +
+                                          std::to_string(need) + " are needed");
   return MUON_OK;
 }
 
@@ -1272,7 +1388,7 @@ int muon_step(muon_handle* h, float* const* params, const void* const* grads, fl
   if ((rc = check_coeffs(coeffs, ns_steps, abc))) return rc;
   DeviceGuard g(h->device);
   if (!g.ok) return fail(MUON_ERR_CUDA, "cudaSetDevice failed");
-  return step_impl(h, params, grads, momenta, shapes, count, lr, beta, nesterov, wd, ns_steps, abc,
+  return step_impl(h, params, grads, momenta, shapes, count, lr, beta, nesterov, wd, ns_steps, abc, nullptr,
                    static_cast<cudaStream_t>(stream));
 }
 
@@ -1289,7 +1405,24 @@ int muon_step_schedule(muon_handle* h, float* const* params, const void* const* 
   if ((rc = check_coeffs(coeff_table, ns_steps, abc, table_rows))) return rc;
   DeviceGuard g(h->device);
   if (!g.ok) return fail(MUON_ERR_CUDA, "cudaSetDevice failed");
-  return step_impl(h, params, grads, momenta, shapes, count, lr, beta, nesterov, wd, ns_steps, abc,
+  return step_impl(h, params, grads, momenta, shapes, count, lr, beta, nesterov, wd, ns_steps, abc, nullptr,
+                   static_cast<cudaStream_t>(stream));
+}
+
+int muon_step_scaled(muon_handle* h, float* const* params, const void* const* grads, float* const* momenta,
+                     const int32_t* shapes, int count, float lr, float beta, int nesterov, float wd, int ns_steps,
+                     const float* coeff_table, int table_rows, const float* grad_scale, void* stream) {
+  g_last_error.clear();
+  int rc;
+  if ((rc = check_common(h, shapes, count))) return rc;
+  if ((rc = check_step_ptrs(params, grads, momenta, shapes, count))) return rc;
+  if ((rc = check_scalars(lr, beta, wd))) return rc;
+  if (reinterpret_cast<uintptr_t>(grad_scale) % 4) return fail(MUON_ERR_INVALID_ARG, "grad_scale is misaligned");
+  float abc[3 * kMaxNsSteps];
+  if ((rc = check_coeffs(coeff_table, ns_steps, abc, coeff_table ? table_rows : 1))) return rc;
+  DeviceGuard g(h->device);
+  if (!g.ok) return fail(MUON_ERR_CUDA, "cudaSetDevice failed");
+  return step_impl(h, params, grads, momenta, shapes, count, lr, beta, nesterov, wd, ns_steps, abc, grad_scale,
                    static_cast<cudaStream_t>(stream));
 }
 
@@ -1314,6 +1447,152 @@ int muon_qk_clip(muon_handle* h, float* const* weights, const int32_t* shapes, c
   for (int i = 0; i < count; ++i)
     MUON_CUDA_TRY(launch_qk_clip(weights[i], shapes[3 * i], shapes[3 * i + 1], shapes[3 * i + 2], s_max[i], tau, st));
   h->last_launches = count;
+  return MUON_OK;
+}
+
+int muon_grad_norm(muon_handle* h, const void* const* tensors, const int64_t* numels, const int32_t* dtypes, int count,
+                   int norm_kind, float max_norm, float* out, float* per_tensor, void* scratch, size_t scratch_bytes,
+                   void* stream) {
+  g_last_error.clear();
+  int rc;
+  long long total = 0;
+  if ((rc = check_list(numels, dtypes, count, "tensors", &total))) return rc;
+  if (count > 0 && !tensors) return fail(MUON_ERR_INVALID_ARG, "tensors is NULL");
+  if ((rc = check_norm_args(norm_kind, max_norm, out, scratch, scratch_bytes, count))) return rc;
+  if (reinterpret_cast<uintptr_t>(per_tensor) % 4) return fail(MUON_ERR_INVALID_ARG, "per_tensor is misaligned");
+  std::vector<GradItem> it((size_t)count);
+  for (int i = 0; i < count; ++i) {
+    const bool skip = tensors[i] == nullptr || numels[i] == 0;
+    if (!skip && (rc = check_elem_ptr(tensors[i], dtype_size(dtypes[i]), "tensors", i))) return rc;
+    it[i] = GradItem{tensors[i], nullptr, skip ? 0 : (long long)numels[i], dtypes[i], dtypes[i]};
+  }
+  if (!h) return fail(MUON_ERR_INVALID_ARG, "handle is NULL");
+  DeviceGuard g(h->device);
+  if (!g.ok) return fail(MUON_ERR_CUDA, "cudaSetDevice failed");
+  prof_call_begin(h);
+  int launches = 0;
+  if ((rc = enqueue_grad_norm(h, it, total, norm_kind, max_norm, out, per_tensor, static_cast<double*>(scratch),
+                              static_cast<cudaStream_t>(stream), &launches)))
+    return rc;
+  h->last_launches = launches;
+  return MUON_OK;
+}
+
+int muon_clip_grads(muon_handle* h, const void* const* src, void* const* dst, const int64_t* numels,
+                    const int32_t* src_dtypes, const int32_t* dst_dtypes, int count, int norm_kind, float max_norm,
+                    float* out, void* scratch, size_t scratch_bytes, void* stream) {
+  g_last_error.clear();
+  int rc;
+  long long total = 0;
+  if ((rc = check_list(numels, src_dtypes, count, "src", &total))) return rc;
+  if ((rc = check_list(numels, dst_dtypes, count, "dst", &total))) return rc;
+  if (count > 0 && (!src || !dst)) return fail(MUON_ERR_INVALID_ARG, "src and dst are required");
+  if ((rc = check_norm_args(norm_kind, max_norm, out, scratch, scratch_bytes, count))) return rc;
+  std::vector<GradItem> it((size_t)count);
+  Ranges ranges;
+  for (int i = 0; i < count; ++i) {
+    const bool skip = src[i] == nullptr || numels[i] == 0;
+    if (!skip) {
+      const size_t ss = dtype_size(src_dtypes[i]), ds = dtype_size(dst_dtypes[i]);
+      if ((rc = check_elem_ptr(src[i], ss, "src", i)) || (rc = check_elem_ptr(dst[i], ds, "dst", i))) return rc;
+      ranges.add(dst[i], (size_t)numels[i] * ds, true);
+      if (src[i] != dst[i]) ranges.add(src[i], (size_t)numels[i] * ss, false);
+      else if (src_dtypes[i] != dst_dtypes[i]) return bad_tensor("dst", i, "is src in another dtype");
+    }
+    it[i] = GradItem{src[i], dst[i], skip ? 0 : (long long)numels[i], src_dtypes[i], dst_dtypes[i]};
+  }
+  if (ranges.clash())
+    return fail(MUON_ERR_INVALID_ARG, "a written tensor overlaps another tensor of the call (the same one twice?)");
+  if (!h) return fail(MUON_ERR_INVALID_ARG, "handle is NULL");
+  DeviceGuard g(h->device);
+  if (!g.ok) return fail(MUON_ERR_CUDA, "cudaSetDevice failed");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_call_begin(h);
+  int launches = 0;
+  if ((rc = enqueue_grad_norm(h, it, total, norm_kind, max_norm, out, nullptr, static_cast<double*>(scratch), st,
+                              &launches)))
+    return rc;
+  const int unit = pick_unit(total, 65536, 4096);
+  // Last tensors first, for what is still in L2 (see g3_scale).
+  for (int i1 = count; i1 > 0; i1 -= kScaleCap) {
+    const int i0 = std::max(0, i1 - kScaleCap), n = i1 - i0;
+    int units = 0;
+    for (int i = i0; i < i1; ++i) units += grad_units(it[i].numel, unit);
+    if (units == 0) continue;
+    const int slot = prof_before(h, MUON_KERNEL_GRAD_SCALE, st);
+    MUON_CUDA_TRY(launch_grad_scale(&it[i0], n, unit, units, out + 1, st));
+    prof_after(h, slot, st);
+    ++launches;
+  }
+  h->last_launches = launches;
+  return MUON_OK;
+}
+
+int muon_adamw_step(muon_handle* h, float* const* params, const void* const* grads, float* const* exp_avgs,
+                    float* const* exp_avg_sqs, const int64_t* numels, const int32_t* grad_dtypes, int count, double lr,
+                    double beta1, double beta2, double eps, double wd, int64_t step, const int64_t* step_dev,
+                    const float* grad_scale, void* stream) {
+  g_last_error.clear();
+  int rc;
+  long long total = 0;
+  if ((rc = check_list(numels, grad_dtypes, count, "grads", &total))) return rc;
+  if (count > 0 && (!params || !grads || !exp_avgs || !exp_avg_sqs))
+    return fail(MUON_ERR_INVALID_ARG, "params, grads, exp_avgs and exp_avg_sqs are required");
+  if (!std::isfinite(lr) || !std::isfinite(wd)) return fail(MUON_ERR_INVALID_ARG, "lr and wd must be finite");
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+    return fail(MUON_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
+  if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(MUON_ERR_INVALID_ARG, "eps must be >= 0 and finite");
+  if (!step_dev && step < 1) return fail(MUON_ERR_INVALID_ARG, "step counts from 1");
+  if (reinterpret_cast<uintptr_t>(step_dev) % 8) return fail(MUON_ERR_INVALID_ARG, "step_dev is misaligned");
+  if (reinterpret_cast<uintptr_t>(grad_scale) % 4) return fail(MUON_ERR_INVALID_ARG, "grad_scale is misaligned");
+  std::vector<AdamItem> it;
+  it.reserve((size_t)count);
+  Ranges ranges;
+  for (int i = 0; i < count; ++i) {
+    if (grads[i] == nullptr || numels[i] == 0) continue;
+    const size_t gs = dtype_size(grad_dtypes[i]), n = (size_t)numels[i];
+    if ((rc = check_elem_ptr(params[i], 4, "params", i)) || (rc = check_elem_ptr(grads[i], gs, "grads", i)) ||
+        (rc = check_elem_ptr(exp_avgs[i], 4, "exp_avgs", i)) ||
+        (rc = check_elem_ptr(exp_avg_sqs[i], 4, "exp_avg_sqs", i)))
+      return rc;
+    ranges.add(params[i], n * 4, true);
+    ranges.add(exp_avgs[i], n * 4, true);
+    ranges.add(exp_avg_sqs[i], n * 4, true);
+    ranges.add(grads[i], n * gs, false);
+    it.push_back(AdamItem{params[i], grads[i], exp_avgs[i], exp_avg_sqs[i], (long long)n, grad_dtypes[i]});
+  }
+  if (ranges.clash())
+    return fail(MUON_ERR_INVALID_ARG, "a written tensor overlaps another tensor of the call (the same one twice?)");
+  if (!h) return fail(MUON_ERR_INVALID_ARG, "handle is NULL");
+  DeviceGuard g(h->device);
+  if (!g.ok) return fail(MUON_ERR_CUDA, "cudaSetDevice failed");
+  AdamArgs a;
+  a.lr = lr;
+  a.beta1 = beta1;
+  a.beta2 = beta2;
+  a.decay = (float)(1.0 - lr * wd);
+  a.eps = (float)eps;
+  a.step = reinterpret_cast<const long long*>(step_dev);
+  a.step_size = a.rsqrt_bc2 = 0.0f;
+  if (!step_dev) {
+    a.step_size = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
+    a.rsqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
+  }
+  a.grad_scale = grad_scale;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_call_begin(h);
+  int launches = 0;
+  const int unit = pick_unit(total, 131072, 2048);
+  for (int i1 = (int)it.size(); i1 > 0; i1 -= kAdamCap) {
+    const int i0 = std::max(0, i1 - kAdamCap), n = i1 - i0;
+    int units = 0;
+    for (int i = i0; i < i1; ++i) units += grad_units(it[i].numel, unit);
+    const int slot = prof_before(h, MUON_KERNEL_ADAMW, st);
+    MUON_CUDA_TRY(launch_adamw(&it[i0], n, unit, units, a, st));
+    prof_after(h, slot, st);
+    ++launches;
+  }
+  h->last_launches = launches;
   return MUON_OK;
 }
 
@@ -1411,7 +1690,7 @@ int muon_step_host(muon_handle* h, float* const* params, const void* const* grad
     MUON_CUDA_TRY(cudaEventRecord(ev_in(c), s_in));
     // Compute.
     MUON_CUDA_TRY(cudaStreamWaitEvent(s_comp, ev_in(c), 0));
-    if ((rc = enqueue_step_range(h, db, hb, chunk_range(P, c), lr, beta, nesterov, wd, ns_steps, abc, s_comp,
+    if ((rc = enqueue_step_range(h, db, hb, chunk_range(P, c), lr, beta, nesterov, wd, ns_steps, abc, nullptr, s_comp,
                                  &launches, d_p_maps)))
       return rc;
     MUON_CUDA_TRY(cudaEventRecord(ev_comp(c), s_comp));
@@ -1467,7 +1746,7 @@ int muon_momentum_norm(muon_handle* h, const void* const* grads, float* const* m
   const ElemLaunch EL = elem_launch(P, static_cast<const MatBind*>(d_binds));
   int slot = prof_before(h, MUON_KERNEL_MOMENTUM_NORM, st);
   MUON_CUDA_TRY(launch_momentum_norm(EL, BUF_OUT, beta, nesterov ? 1 : 0, sumsq, P.partials, h->status,
-                                     h->cfg.check_nonfinite, h->cfg.ns_precision == MUON_NS_FP32, st));
+                                     h->cfg.check_nonfinite, h->cfg.ns_precision == MUON_NS_FP32, nullptr, st));
   prof_after(h, slot, st);
   h->last_launches = 1;
   if (P.partials) {
