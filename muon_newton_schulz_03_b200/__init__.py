@@ -28,10 +28,10 @@ from __future__ import annotations
 import ctypes
 import math
 
-from ._lib import EXPORTED, MuonConfig, MuonError, check, lib_path, load
+from ._lib import EXPORTED, MuonConfig, MuonError, check, lib_path, load, load_lists
 
 __all__ = ["Muon", "MuonError", "plan_query", "x_layout", "round_up", "split_rows", "SCALE_MODES",
-           "DEFAULT_COEFFS", "EXPORTED", "lib_path", "load"]
+           "DEFAULT_COEFFS", "EXPORTED", "lib_path", "load", "load_lists"]
 
 DEFAULT_COEFFS = (3.4445, -4.7750, 2.0315)
 SCALE_MODES = {"moonlight": 0, "jordan": 1, "bernstein": 2, "none": 3}
@@ -39,7 +39,6 @@ PRECISIONS = {"bf16": 0, "fp32": 1}
 ALGORITHMS = {"standard": 0, "gram": 1}
 FLAG_GRAD_BF16 = 1
 NORM_KINDS = {2: 0, math.inf: 1}
-GRAD_SCRATCH_DOUBLES = 32768    # MUON_GRAD_SCRATCH_BYTES(count) = 8 * (32768 + count)
 
 
 def round_up(x: int, k: int) -> int:
@@ -148,15 +147,13 @@ def _marshal_step(params, grads, momenta, host=False, device_index=None):
 
 # -- lists of tensors of any shape ------------------------------------------
 
-_GRAD_DTYPES = None
-
-
 def _grad_dtypes():
-    global _GRAD_DTYPES
-    if _GRAD_DTYPES is None:
-        import torch
-        _GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    return _GRAD_DTYPES
+    import torch
+    return torch.float32, torch.bfloat16, torch.float16
+
+
+def _sequence(ts):
+    return ts if isinstance(ts, (list, tuple)) else list(ts)
 
 
 def _dense(t):
@@ -190,33 +187,27 @@ def _check_tensor(t, what, dtypes, device, like=None):
             raise ValueError(f"{what} has strides {t.stride()}, its partner {like.stride()}")
     if t.device.type != "cuda" or t.device.index != device:
         raise ValueError(f"{what} must be on cuda:{device}, got {t.device}")
+    if t.numel() and not t.data_ptr():
+        raise ValueError(f"{what} has no memory")
 
 
-def _marshal_lists(device, dtypes, lists):
-    """Pointer arrays, element counts and types of paired tensor lists.
+def _bad_lists(device, lists):
+    """Raise the precise error for paired tensor lists that the reader (csrc/python/lists.cpp) refused.
 
-    ``lists`` is [(name, tensors, allowed dtypes), ...]; where an entry of
-    the first is None, the entry is skipped (its partners are not looked at).
-    Returns ([pointer array per list], numels, [type array per list], count).
+    ``lists`` is [(name, tensors, allowed dtypes), ...]; an entry whose first
+    is None is skipped (its partners are not looked at).
     """
     first = lists[0][1]
-    n = len(first)
     for name, ts, _ in lists[1:]:
-        if len(ts) != n:
-            raise ValueError(f"{name} has {len(ts)} entries, {lists[0][0]} has {n}")
-    numels = (ctypes.c_int64 * n)()
-    ptrs = [(ctypes.c_void_p * n)() for _ in lists]
-    types = [(ctypes.c_int32 * n)() for _ in lists]
+        if len(ts) != len(first):
+            raise ValueError(f"{name} has {len(ts)} entries, {lists[0][0]} has {len(first)}")
     for i, t in enumerate(first):
         if t is None:
             continue
-        for (name, ts, allowed), pa, ta in zip(lists, ptrs, types):
+        for name, ts, allowed in lists:
             x = ts[i]
             _check_tensor(x, f"{name}[{i}]", allowed, device, None if x is t else t)
-            pa[i] = x.data_ptr()
-            ta[i] = dtypes[x.dtype]
-        numels[i] = t.numel()
-    return ptrs, numels, types, n
+    raise ValueError(f"{lists[0][0]}: invalid tensors")   # not reached
 
 
 def _check_scalar(t, what, dtype, device):
@@ -349,6 +340,8 @@ class Muon:
         h = ctypes.c_void_p()
         check(self._lib.muon_init(int(device), ctypes.byref(cfg), ctypes.byref(h)))
         self._h = h
+        self._hv = h.value
+        self._lists = load_lists()
         self.device = device
         self.ns_precision = ns_precision
         self.small_path = bool(small_path)
@@ -365,6 +358,7 @@ class Muon:
         if getattr(self, "_h", None):
             self._lib.muon_destroy(self._h)
             self._h = None
+            self._hv = 0
 
     def __del__(self):
         try:
@@ -423,19 +417,12 @@ class Muon:
                                          _stream_handle(stream)))
 
     # -- gradients of the whole model, and the tensors Muon does not take ----
-    def _stream_of(self, stream):
-        """The torch stream of a call: the one given, else the current one of the handle's device."""
+    def _on(self, stream):
+        """Context in which the given stream is the current one."""
         import torch
-        return torch.cuda.current_stream(self.device) if stream is None else stream
-
-    def _grad_buffers(self, count, per_tensor, stream):
-        """Results and scratch of a norm, from the call's stream's memory."""
-        import torch
-        with torch.cuda.stream(stream):
-            out = torch.empty(2, dtype=torch.float32, device=f"cuda:{self.device}")
-            per = torch.empty(count, dtype=torch.float32, device=out.device) if per_tensor else None
-            scratch = torch.empty(GRAD_SCRATCH_DOUBLES + count, dtype=torch.float64, device=out.device)
-        return out, per, scratch
+        if stream.device.index != self.device:
+            raise ValueError(f"stream must be on cuda:{self.device}, got {stream.device}")
+        return torch.cuda.stream(stream)
 
     def grad_norm(self, tensors, max_norm=None, norm_type=2.0, per_tensor=False, stream=None):
         """Norm of all the tensors together and its clip multiplier, on the device.
@@ -448,15 +435,17 @@ class Muon:
         pass ``scale`` on as ``grad_scale``. A NaN or infinity among the
         entries makes the norm NaN or infinite, the multiplier NaN or 0.
         """
-        kind = _norm_kind(norm_type)
-        types = _grad_dtypes()
-        (pa,), na, (ta,), n = _marshal_lists(self.device, types, [("tensors", list(tensors), types)])
-        st = self._stream_of(stream)
-        out, per, scratch = self._grad_buffers(n, per_tensor, st)
-        check(self._lib.muon_grad_norm(self._h, pa, na, ta, n, kind, math.inf if max_norm is None else float(max_norm),
-                                       out.data_ptr(), _ptr(per), scratch.data_ptr(), 8 * scratch.numel(),
-                                       _stream_handle(st)))
-        return (out[0], out[1], per) if per_tensor else (out[0], out[1])
+        if stream is not None:
+            with self._on(stream):
+                return self.grad_norm(tensors, max_norm, norm_type, per_tensor)
+        tensors = _sequence(tensors)
+        r = self._lists.grad_norm(self._hv, self.device, tensors, _norm_kind(norm_type),
+                                  math.inf if max_norm is None else max_norm, per_tensor)
+        if r is None:
+            _bad_lists(self.device, [("tensors", tensors, _grad_dtypes())])
+        if isinstance(r, int):
+            check(r)
+        return r
 
     def clip_grads(self, grads, max_norm, norm_type=2.0, out=None, stream=None):
         """Multiply the gradients by min(1, max_norm / (norm + 1e-6)); returns the norm before (float32 CUDA scalar).
@@ -464,16 +453,17 @@ class Muon:
         In place, or into the tensors of ``out`` (same shapes and strides,
         fp32, bf16 or fp16). ``grads`` as in ``grad_norm``; no tensor twice.
         """
-        kind = _norm_kind(norm_type)
-        types = _grad_dtypes()
-        grads = list(grads)
-        (sa, da), na, (st_, dt), n = _marshal_lists(
-            self.device, types, [("grads", grads, types), ("out", grads if out is None else list(out), types)])
-        st = self._stream_of(stream)
-        res, _, scratch = self._grad_buffers(n, False, st)
-        check(self._lib.muon_clip_grads(self._h, sa, da, na, st_, dt, n, kind, float(max_norm), res.data_ptr(),
-                                        scratch.data_ptr(), 8 * scratch.numel(), _stream_handle(st)))
-        return res[0]
+        if stream is not None:
+            with self._on(stream):
+                return self.clip_grads(grads, max_norm, norm_type, out)
+        grads = _sequence(grads)
+        to = grads if out is None else _sequence(out)
+        r = self._lists.clip_grads(self._hv, self.device, grads, to, _norm_kind(norm_type), max_norm)
+        if r is None:
+            _bad_lists(self.device, [("grads", grads, _grad_dtypes()), ("out", to, _grad_dtypes())])
+        if isinstance(r, int):
+            check(r)
+        return r
 
     def adamw_step(self, params, grads, exp_avgs, exp_avg_sqs, lr, step, betas=(0.9, 0.999), eps=1e-8, wd=0.1,
                    grad_scale=None, stream=None):
@@ -486,18 +476,21 @@ class Muon:
         that a captured step reads at every replay (the caller advances it).
         ``grad_scale``: as in ``step``.
         """
+        if stream is not None:
+            with self._on(stream):
+                return self.adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr, step, betas, eps, wd, grad_scale)
         import torch
-        types = _grad_dtypes()
-        f32 = (torch.float32,)
-        (ga, pa, ma, va), na, (ta, *_), n = _marshal_lists(
-            self.device, types, [("grads", list(grads), types), ("params", list(params), f32),
-                                 ("exp_avgs", list(exp_avgs), f32), ("exp_avg_sqs", list(exp_avg_sqs), f32)])
-        on_device = isinstance(step, torch.Tensor)
-        check(self._lib.muon_adamw_step(
-            self._h, pa, ga, ma, va, na, ta, n, float(lr), float(betas[0]), float(betas[1]), float(eps), float(wd),
-            0 if on_device else int(step), _check_scalar(step, "step", torch.int64, self.device) if on_device else None,
-            _check_scalar(grad_scale, "grad_scale", torch.float32, self.device),
-            _stream_handle(self._stream_of(stream))))
+        lists = [_sequence(ts) for ts in (grads, params, exp_avgs, exp_avg_sqs)]
+        at = 0
+        if isinstance(step, torch.Tensor):
+            step, at = 0, _check_scalar(step, "step", torch.int64, self.device)
+        r = self._lists.adamw_step(self._hv, self.device, *lists, lr, betas[0], betas[1], eps, wd, step, at,
+                                   _check_scalar(grad_scale, "grad_scale", torch.float32, self.device) or 0)
+        if r is None:
+            f32 = (torch.float32,)
+            _bad_lists(self.device, [("grads", lists[0], _grad_dtypes()), ("params", lists[1], f32),
+                                     ("exp_avgs", lists[2], f32), ("exp_avg_sqs", lists[3], f32)])
+        check(r)
 
     def qk_clip(self, weights, s_max, head_rows, tau=100.0, stream=None):
         """QK-Clip in place on W_q / W_k weights (fp32 CUDA tensors).

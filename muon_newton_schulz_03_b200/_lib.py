@@ -111,6 +111,28 @@ def load():
         return lib
 
 
+_LISTS = None
+
+
+def load_lists():
+    """Load (building first if needed) the list reader, bound to the C functions."""
+    global _LISTS
+    if _LISTS is not None:
+        return _LISTS
+    lib = load()
+    with _LOCK:
+        if _LISTS is None:
+            if _build.lists_need_build():
+                _build.build_lists()
+            import torch  # noqa: F401  (its libraries, before the module that uses them)
+
+            from . import _lists
+            _lists.bind(*(ctypes.cast(getattr(lib, f), c_void_p).value
+                          for f in ("muon_grad_norm", "muon_clip_grads", "muon_adamw_step")))
+            _LISTS = _lists
+    return _LISTS
+
+
 class MuonError(RuntimeError):
     """A non-zero status from the C ABI."""
 

@@ -1,0 +1,228 @@
+// Python side of the list operators: reads lists of torch tensors and makes
+// the C calls of include/muon_ns.h.
+//
+// A whole model is hundreds of tensors and four lists of them, so reading
+// each tensor's attributes through the interpreter (about 2 us a tensor)
+// costs several times the kernels. Here a tensor takes tens of nanoseconds.
+// A list that does not pass returns None, and the binding says what is wrong
+// with it; a C error comes back as its status code. Nothing is kept between
+// calls.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <vector>
+
+#include "muon_ns.h"
+
+namespace {
+
+decltype(&muon_grad_norm) c_norm = nullptr;
+decltype(&muon_clip_grads) c_clip = nullptr;
+decltype(&muon_adamw_step) c_adamw = nullptr;
+
+constexpr int kAny = 7, kF32 = 1;   // allowed types, one bit each
+
+struct Column {
+  std::vector<void*> ptr;
+  std::vector<int32_t> type;
+  void resize(size_t n) {
+    ptr.assign(n, nullptr);
+    type.assign(n, 0);
+  }
+};
+
+int type_of(const at::Tensor& t) {
+  switch (t.scalar_type()) {
+    case at::kFloat: return MUON_DTYPE_F32;
+    case at::kBFloat16: return MUON_DTYPE_BF16;
+    case at::kHalf: return MUON_DTYPE_F16;
+    default: return -1;
+  }
+}
+
+// A dense strided tensor of an allowed type on the device, laid out like `like`.
+bool take(PyObject* o, int64_t device, int allowed, const at::Tensor* like, Column& c, size_t i) {
+  if (!THPVariable_Check(o)) return false;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (t.layout() != at::kStrided || !t.is_cuda() || t.get_device() != device || t.is_neg()) return false;
+  const int type = type_of(t);
+  if (type < 0 || !((allowed >> type) & 1)) return false;
+  const bool contiguous = t.is_contiguous();
+  if (!contiguous && !t.unsafeGetTensorImpl()->is_non_overlapping_and_dense()) return false;
+  if (like != nullptr) {
+    if (t.sizes() != like->sizes()) return false;
+    if (!(contiguous && like->is_contiguous()) && t.strides() != like->strides()) return false;
+  }
+  c.ptr[i] = t.data_ptr();
+  c.type[i] = type;
+  return c.ptr[i] != nullptr || t.numel() == 0;
+}
+
+// Paired lists; where the first holds None, the entry is skipped.
+struct Lists {
+  static constexpr int kMost = 4;
+  PyObject* seq[kMost] = {};
+  Column col[kMost];
+  std::vector<int64_t> numel;
+  int n = 0;
+  ~Lists() {
+    for (PyObject* s : seq) Py_XDECREF(s);
+  }
+  bool read(PyObject* const* lists, const int* allowed, int count, int64_t device) {
+    for (int k = 0; k < count; ++k) {
+      seq[k] = PySequence_Fast(lists[k], "a list of tensors is needed");
+      if (!seq[k]) {
+        PyErr_Clear();
+        return false;
+      }
+      if (PySequence_Fast_GET_SIZE(seq[k]) != PySequence_Fast_GET_SIZE(seq[0])) return false;
+    }
+    const Py_ssize_t size = PySequence_Fast_GET_SIZE(seq[0]);
+    if (size > INT32_MAX) return false;
+    n = (int)size;
+    numel.assign((size_t)n, 0);
+    for (int k = 0; k < count; ++k) col[k].resize((size_t)n);
+    for (int i = 0; i < n; ++i) {
+      PyObject* o = PySequence_Fast_GET_ITEM(seq[0], i);
+      if (o == Py_None) continue;
+      if (!take(o, device, allowed[0], nullptr, col[0], (size_t)i)) return false;
+      const at::Tensor& t = THPVariable_Unpack(o);
+      numel[i] = t.numel();
+      for (int k = 1; k < count; ++k)
+        if (!take(PySequence_Fast_GET_ITEM(seq[k], i), device, allowed[k], &t, col[k], (size_t)i)) return false;
+    }
+    return true;
+  }
+};
+
+// Runs `body`, with C++ exceptions as Python ones.
+template <class F>
+PyObject* guarded(F body) {
+  try {
+    return body();
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
+bool want_args(Py_ssize_t got, Py_ssize_t want) {
+  if (got == want) return true;
+  PyErr_Format(PyExc_TypeError, "%zd arguments are needed, got %zd", want, got);
+  return false;
+}
+
+muon_handle* handle_of(PyObject* o) { return static_cast<muon_handle*>(PyLong_AsVoidPtr(o)); }
+
+// Results and scratch, from the memory of the stream that the call runs on.
+struct Buffers {
+  at::Tensor out, per, scratch;
+  size_t bytes;
+  Buffers(int64_t device, int n, bool per_tensor) {
+    const auto on = at::TensorOptions().device(at::kCUDA, (c10::DeviceIndex)device);
+    bytes = MUON_GRAD_SCRATCH_BYTES(n);
+    out = at::empty({2}, on.dtype(at::kFloat));
+    if (per_tensor) per = at::empty({n}, on.dtype(at::kFloat));
+    scratch = at::empty({(int64_t)(bytes / 8)}, on.dtype(at::kDouble));
+  }
+};
+
+// bind(norm, clip, adamw): addresses of the C functions.
+PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!want_args(n, 3)) return nullptr;
+  c_norm = reinterpret_cast<decltype(c_norm)>(PyLong_AsVoidPtr(a[0]));
+  c_clip = reinterpret_cast<decltype(c_clip)>(PyLong_AsVoidPtr(a[1]));
+  c_adamw = reinterpret_cast<decltype(c_adamw)>(PyLong_AsVoidPtr(a[2]));
+  if (PyErr_Occurred()) return nullptr;
+  Py_RETURN_NONE;
+}
+
+// grad_norm(handle, device, tensors, norm_kind, max_norm, per_tensor)
+//   -> (norm, scale), (norm, scale, per_tensor), a status code, or None
+PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  if (!want_args(nargs, 6)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    muon_handle* h = handle_of(a[0]);
+    const int64_t device = PyLong_AsLongLong(a[1]);
+    const int kind = (int)PyLong_AsLong(a[3]);
+    const float max_norm = (float)PyFloat_AsDouble(a[4]);
+    const bool per = PyObject_IsTrue(a[5]) == 1;
+    if (PyErr_Occurred()) return nullptr;
+    Lists l;
+    const int allowed[1] = {kAny};
+    if (!l.read(&a[2], allowed, 1, device)) Py_RETURN_NONE;
+    Buffers b(device, l.n, per);
+    const int rc = c_norm(h, l.col[0].ptr.data(), l.numel.data(), l.col[0].type.data(), l.n, kind, max_norm,
+                          b.out.data_ptr<float>(), per ? b.per.data_ptr<float>() : nullptr, b.scratch.data_ptr(),
+                          b.bytes, c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
+    if (rc) return PyLong_FromLong(rc);
+    PyObject* r = PyTuple_New(per ? 3 : 2);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(b.out.select(0, 0)));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(b.out.select(0, 1)));
+    if (per) PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(b.per));
+    return r;
+  });
+}
+
+// clip_grads(handle, device, grads, out, norm_kind, max_norm) -> norm, a status code, or None
+PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  if (!want_args(nargs, 6)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    muon_handle* h = handle_of(a[0]);
+    const int64_t device = PyLong_AsLongLong(a[1]);
+    const int kind = (int)PyLong_AsLong(a[4]);
+    const float max_norm = (float)PyFloat_AsDouble(a[5]);
+    if (PyErr_Occurred()) return nullptr;
+    Lists l;
+    const int allowed[2] = {kAny, kAny};
+    if (!l.read(&a[2], allowed, 2, device)) Py_RETURN_NONE;
+    Buffers b(device, l.n, false);
+    const int rc = c_clip(h, l.col[0].ptr.data(), l.col[1].ptr.data(), l.numel.data(), l.col[0].type.data(),
+                          l.col[1].type.data(), l.n, kind, max_norm, b.out.data_ptr<float>(), b.scratch.data_ptr(),
+                          b.bytes, c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
+    if (rc) return PyLong_FromLong(rc);
+    return THPVariable_Wrap(b.out.select(0, 0));
+  });
+}
+
+// adamw_step(handle, device, grads, params, exp_avgs, exp_avg_sqs, lr, beta1, beta2, eps, wd, step, step_dev,
+//            grad_scale) -> a status code, or None; step_dev and grad_scale are addresses (0: none)
+PyObject* py_adamw(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  if (!want_args(nargs, 14)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    muon_handle* h = handle_of(a[0]);
+    const int64_t device = PyLong_AsLongLong(a[1]);
+    double x[5];
+    for (int k = 0; k < 5; ++k) x[k] = PyFloat_AsDouble(a[6 + k]);
+    const int64_t step = PyLong_AsLongLong(a[11]);
+    const void* step_dev = PyLong_AsVoidPtr(a[12]);
+    const void* scale = PyLong_AsVoidPtr(a[13]);
+    if (PyErr_Occurred()) return nullptr;
+    Lists l;
+    const int allowed[4] = {kAny, kF32, kF32, kF32};
+    if (!l.read(&a[2], allowed, 4, device)) Py_RETURN_NONE;
+    const auto f = [&](int k) { return reinterpret_cast<float* const*>(l.col[k].ptr.data()); };
+    const int rc = c_adamw(h, f(1), l.col[0].ptr.data(), f(2), f(3), l.numel.data(), l.col[0].type.data(), l.n, x[0],
+                           x[1], x[2], x[3], x[4], step, static_cast<const int64_t*>(step_dev),
+                           static_cast<const float*>(scale),
+                           c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
+    return PyLong_FromLong(rc);
+  });
+}
+
+#define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL
+PyMethodDef methods[] = {{"bind", FAST(py_bind), nullptr},
+                         {"grad_norm", FAST(py_norm), nullptr},
+                         {"clip_grads", FAST(py_clip), nullptr},
+                         {"adamw_step", FAST(py_adamw), nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lists", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__lists(void) { return PyModule_Create(&module); }

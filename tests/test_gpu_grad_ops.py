@@ -424,6 +424,24 @@ def test_refusals_on_the_device(opt):
         opt.adamw_step([a], [b], [b.clone()], [b.clone()], lr=1e-3, step=torch.ones(1, device=DEV))
 
 
+def test_a_closed_handle_is_refused():
+    o = muon.Muon(device=0)
+    a = torch.zeros(4, device=DEV)
+    o.close()
+    for call in (lambda: o.grad_norm([a]), lambda: o.clip_grads([a], 1.0),
+                 lambda: o.adamw_step([a], [a.clone()], [a.clone()], [a.clone()], lr=1e-3, step=1)):
+        with pytest.raises(muon.MuonError) as e:
+            call()
+        assert "handle is NULL" in str(e.value)
+
+
+def test_lists_of_other_kinds(opt):
+    a, b = tensors([100, 50], (F32,))
+    want = exact_norm([a, b])[0]
+    for ts in ((a, b), iter([a, b]), {"a": a, "b": b}.values()):
+        assert abs(opt.grad_norm(ts)[0].item() - want) <= U * 1.001 * want
+
+
 @pytest.mark.parametrize("dtype", [BF16])
 def test_more_than_2_to_31_elements(opt, dtype):
     n = (1 << 31) + 4099

@@ -12,9 +12,9 @@ import pytest
 import torch
 
 import muon_newton_schulz_03_b200 as muon
-from muon_newton_schulz_03_b200 import (GRAD_SCRATCH_DOUBLES, _check_scalar, _dense, _grad_dtypes, _marshal_lists,
-                                        _norm_kind)
+from muon_newton_schulz_03_b200 import _bad_lists, _check_scalar, _dense, _grad_dtypes, _norm_kind
 
+GRAD_SCRATCH_DOUBLES = 32768   # MUON_GRAD_SCRATCH_BYTES(count) = 8 * (32768 + count)
 BASE = 1 << 20      # made-up device addresses: nothing reads them
 SCRATCH = 8 * (GRAD_SCRATCH_DOUBLES + 16)
 
@@ -119,9 +119,14 @@ def test_step_scaled_refuses_a_null_handle():
 #    tensors in host memory reach every check
 
 def _marshal(ts, *more, device=0):
-    types = _grad_dtypes()
-    return _marshal_lists(device, types, [("grads", ts, types)] + [(f"more{k}", m, (torch.float32,))
-                                                                   for k, m in enumerate(more)])
+    """What the binding does with a list: the reader refuses it, then the reason is raised."""
+    reader = muon.load_lists()
+    if not more:
+        assert reader.grad_norm(0, device, ts, 0, 1.0, False) is None
+    else:
+        assert reader.adamw_step(0, device, ts, *(list(more) * 3)[:3], 1e-3, 0.9, 0.999, 1e-8, 0.0, 1, 0, 0) is None
+    _bad_lists(device, [("grads", ts, _grad_dtypes())] + [(f"more{k}", m, (torch.float32,))
+                                                          for k, m in enumerate(more)])
 
 
 @pytest.mark.parametrize("bad,exc,msg", [
@@ -178,3 +183,15 @@ def test_binding_refuses_scalars(t):
     (torch.zeros(3, 1).expand(3, 2), False), (torch.zeros(5, 4)[1:3], True), (torch.zeros(4, 4)[:, :1], False)])
 def test_dense(t, ok):
     assert _dense(t) is ok
+
+
+def test_reader_refuses_bad_arguments():
+    reader = muon.load_lists()
+    for bad in (5, None, [None]):
+        assert reader.adamw_step(0, 0, bad, [], [], [], 1e-3, 0.9, 0.999, 1e-8, 0.0, 1, 0, 0) is None
+    with pytest.raises(TypeError):
+        reader.grad_norm(0, 0)
+    with pytest.raises(TypeError):
+        reader.adamw_step(0, 0, [], [], [], [], "x", 0.9, 0.999, 1e-8, 0.0, 1, 0, 0)
+    with pytest.raises(TypeError):
+        reader.clip_grads("handle", 0, [], [], 0, 1.0)
