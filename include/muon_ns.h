@@ -460,7 +460,8 @@ enum muon_kernel_kind {
   MUON_KERNEL_GRAD_NORM = 10,    /* partial norms of a list of gradients      */
   MUON_KERNEL_GRAD_FINISH = 11,  /* their sum, the clip multiplier            */
   MUON_KERNEL_GRAD_SCALE = 12,   /* clipped copy                              */
-  MUON_KERNEL_ADAMW = 13         /* AdamW update of a list of tensors         */
+  MUON_KERNEL_ADAMW = 13,        /* AdamW update of a list of tensors         */
+  MUON_KERNEL_GRAD_SMALL = 14    /* norm (and clipped copy) of a small list   */
 };
 
 /* Per-launch timing for measurements. With max_calls > 0, each of the next

@@ -607,7 +607,7 @@ class Muon:
         return base.value or 0, size.value
 
     KERNEL_KINDS = ("momentum_norm", "ns_gram", "ns_poly", "ns_comb", "apply", "scale_copy", "ns_fp32", "ns_small",
-                    "norm_reduce", "ns_sym", "grad_norm", "grad_finish", "grad_scale", "adamw")
+                    "norm_reduce", "ns_sym", "grad_norm", "grad_finish", "grad_scale", "adamw", "grad_small")
 
     def profile_enable(self, max_calls: int):
         """Record CUDA events around every kernel of the next max_calls calls."""

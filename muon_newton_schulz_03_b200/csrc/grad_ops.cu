@@ -117,6 +117,7 @@ template <> struct Elem<GRAD_F16> {
 struct SumSq {
   double v;
   static __device__ __forceinline__ SumSq zero() { return SumSq{0.0}; }
+  static __device__ __forceinline__ SumSq load(const SumSq* p) { return SumSq{__ldcg(&p->v)}; }
   template <int kType> __device__ __forceinline__ void add(const float* x) {
     if constexpr (kType == GRAD_F32) {
       // fp64 per element: an fp32 square can overflow or vanish.
@@ -149,6 +150,7 @@ struct SumSq {
 struct MaxAbs {
   unsigned long long v;   // as wide as SumSq: they share the partials' array
   static __device__ __forceinline__ MaxAbs zero() { return MaxAbs{0}; }
+  static __device__ __forceinline__ MaxAbs load(const MaxAbs* p) { return MaxAbs{__ldcg(&p->v)}; }
   template <int kType> __device__ __forceinline__ void add(const float* x) {
 #pragma unroll
     for (int k = 0; k < Elem<kType>::kVec; ++k) add1(x[k]);
@@ -183,10 +185,10 @@ __device__ __forceinline__ Acc block_join(Acc a) {
   return t;
 }
 
-// Elements [e0, e1) of a tensor: scalars up to the first 16-byte boundary,
-// then vectors, four in flight per thread, then the rest.
-template <class Acc, int kType>
-__device__ __forceinline__ Acc unit_norm(const void* base, long long e0, long long e1) {
+// Elements [e0, e1) of a tensor by kStride threads: scalars up to the first
+// 16-byte boundary, then vectors, four in flight per thread, then the rest.
+template <class Acc, int kType, int kStride>
+__device__ __forceinline__ Acc unit_norm(const void* base, long long e0, long long e1, int tid) {
   typedef Elem<kType> E;
   typedef typename E::T T;
   Acc a = Acc::zero();
@@ -195,11 +197,11 @@ __device__ __forceinline__ Acc unit_norm(const void* base, long long e0, long lo
   const int head = (int)min((long long)(((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T)), n);
   const long long nv = (n - head) / E::kVec;
   const uint4* q = reinterpret_cast<const uint4*>(p + head);
-  long long i = threadIdx.x;
-  for (; i + 3 * kThreads < nv; i += 4 * kThreads) {
+  long long i = tid;
+  for (; i + 3 * kStride < nv; i += 4 * kStride) {
     uint4 r[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = __ldg(q + i + k * kThreads);
+    for (int k = 0; k < 4; ++k) r[k] = q[i + k * kStride];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float x[E::kVec];
@@ -207,34 +209,37 @@ __device__ __forceinline__ Acc unit_norm(const void* base, long long e0, long lo
       a.template add<kType>(x);
     }
   }
-  for (; i < nv; i += kThreads) {
+  for (; i < nv; i += kStride) {
     float x[E::kVec];
-    E::unpack(__ldg(q + i), x);
+    E::unpack(q[i], x);
     a.template add<kType>(x);
   }
-  if ((int)threadIdx.x < head) a.add1(E::get(p, threadIdx.x));
-  const long long t = head + nv * E::kVec + threadIdx.x;
+  if (tid < head) a.add1(E::get(p, tid));
+  const long long t = head + nv * E::kVec + tid;
   if (t < n) a.add1(E::get(p, t));
   return a;
+}
+
+template <class Acc, int kStride>
+__device__ __forceinline__ Acc unit_norm(int type, const void* base, long long e0, long long e1, int tid) {
+  switch (type) {
+    case GRAD_F32: return unit_norm<Acc, GRAD_F32, kStride>(base, e0, e1, tid);
+    case GRAD_BF16: return unit_norm<Acc, GRAD_BF16, kStride>(base, e0, e1, tid);
+    default: return unit_norm<Acc, GRAD_F16, kStride>(base, e0, e1, tid);
+  }
 }
 
 template <class Acc, int kCap>
 __global__ void __launch_bounds__(kThreads) g1_norm(const __grid_constant__ GradTable<kCap> t, int unit,
                                                     Acc* __restrict__ partials) {
-  dep_wait();
-  dep_release();
   const int blk = blockIdx.x;
   const int i = find_tensor(t.unit0, t.count, blk);
   const unsigned long long meta = t.meta[i];
   const long long e0 = (long long)(blk - t.unit0[i]) * unit;
   const long long e1 = min(e0 + unit, grad_numel(meta));
-  Acc a = Acc::zero();
-  switch (grad_src(meta)) {
-    case GRAD_F32: a = unit_norm<Acc, GRAD_F32>(t.src[i], e0, e1); break;
-    case GRAD_BF16: a = unit_norm<Acc, GRAD_BF16>(t.src[i], e0, e1); break;
-    default: a = unit_norm<Acc, GRAD_F16>(t.src[i], e0, e1); break;
-  }
-  a = block_join<Acc, kThreads>(a);
+  dep_wait();
+  dep_release();
+  const Acc a = block_join<Acc, kThreads>(unit_norm<Acc, kThreads>(grad_src(meta), t.src[i], e0, e1, threadIdx.x));
   if (threadIdx.x == 0) partials[blk] = a;
 }
 
@@ -245,29 +250,45 @@ __device__ __forceinline__ float clip_scale(double norm, float max_norm) {
   return c >= 1.0 ? 1.0f : (float)c;
 }
 
-// Block 0 (of the launch that has `out`): the norm of everything and its clip
-// multiplier. Other blocks: one warp per tensor adds its units' partials.
+// All partials, by one block; valid in thread 0.
+template <class Acc, int kBlock>
+__device__ __forceinline__ Acc join_partials(const Acc* all, long long nunits) {
+  Acc a = Acc::zero();
+  long long i = threadIdx.x;
+  for (; i + 7 * kBlock < nunits; i += 8 * kBlock) {
+    Acc b[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) b[k] = Acc::load(all + i + k * kBlock);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a.join(b[k]);
+  }
+  for (; i < nunits; i += kBlock) a.join(Acc::load(all + i));
+  return block_join<Acc, kBlock>(a);
+}
+
+// One tensor's norm from its units' partials, by one warp.
 template <class Acc>
-__global__ void __launch_bounds__(kFinishThreads) g2_finish(const __grid_constant__ SpanTable t,
-                                                            const Acc* __restrict__ all, long long nunits,
-                                                            float max_norm, float* __restrict__ out,
-                                                            const Acc* __restrict__ partials,
+__device__ __forceinline__ void tensor_norm(const int* unit0, int i, const Acc* partials, float* per_tensor) {
+  const int lane = threadIdx.x & 31;
+  Acc a = Acc::zero();
+  for (int u = unit0[i] + lane; u < unit0[i + 1]; u += 32) a.join(Acc::load(partials + u));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a.join(a.peer(o));
+  if (lane == 0) per_tensor[i] = (float)a.norm();
+}
+
+// Block 0 (of the launch that has `out`): the norm of everything and its clip
+// multiplier. Other blocks: a warp per tensor.
+template <class Acc, int kCap>
+__global__ void __launch_bounds__(kFinishThreads) g2_finish(const __grid_constant__ SpanTable<kCap> t,
+                                                            const Acc* all, long long nunits, float max_norm,
+                                                            float* __restrict__ out, const Acc* partials,
                                                             float* __restrict__ per_tensor) {
   dep_wait();
   dep_release();
   if (blockIdx.x == 0) {
     if (out == nullptr) return;
-    Acc a = Acc::zero();
-    long long i = threadIdx.x;
-    for (; i + 7 * kFinishThreads < nunits; i += 8 * kFinishThreads) {
-      Acc b[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) b[k] = all[i + k * kFinishThreads];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) a.join(b[k]);
-    }
-    for (; i < nunits; i += kFinishThreads) a.join(all[i]);
-    a = block_join<Acc, kFinishThreads>(a);
+    const Acc a = join_partials<Acc, kFinishThreads>(all, nunits);
     if (threadIdx.x == 0) {
       const double norm = a.norm();
       out[0] = (float)norm;
@@ -276,13 +297,7 @@ __global__ void __launch_bounds__(kFinishThreads) g2_finish(const __grid_constan
     return;
   }
   const int i = (int)(blockIdx.x - 1) * (kFinishThreads / 32) + (int)(threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (i >= t.count) return;
-  Acc a = Acc::zero();
-  for (int u = t.unit0[i] + lane; u < t.unit0[i + 1]; u += 32) a.join(partials[u]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a.join(a.peer(o));
-  if (lane == 0) per_tensor[i] = (float)a.norm();
+  if (i < t.count) tensor_norm(t.unit0, i, partials, per_tensor);
 }
 
 // ---------------------------------------------------------------------------
@@ -292,8 +307,9 @@ __global__ void __launch_bounds__(kFinishThreads) g2_finish(const __grid_constan
 // dst[e0..e1) = s * src, each rounded once to dst's type. `phase` elements
 // bring both to a 16-byte boundary at every unit (units are multiples of 8);
 // kNoPhase: no such number, so elements go one by one.
-template <int kSrc, int kDst>
-__device__ __forceinline__ void unit_scale(const void* src, void* dst, long long e0, long long e1, int phase, float s) {
+template <int kSrc, int kDst, int kStride>
+__device__ __forceinline__ void unit_scale(const void* src, void* dst, long long e0, long long e1, int phase, float s,
+                                           int tid) {
   typedef Elem<kSrc> S;
   typedef Elem<kDst> D;
   constexpr int kStep = 8;
@@ -304,7 +320,7 @@ __device__ __forceinline__ void unit_scale(const void* src, void* dst, long long
     const uint4* in = reinterpret_cast<const uint4*>(static_cast<const typename S::T*>(src) + e0 + head);
     uint4* out = reinterpret_cast<uint4*>(static_cast<typename D::T*>(dst) + e0 + head);
     constexpr int kIn = kStep / S::kVec, kOut = kStep / D::kVec;
-    for (long long i = threadIdx.x; i < nv; i += kThreads) {
+    for (long long i = tid; i < nv; i += kStride) {
       float x[kStep];
       uint4 r[kIn];
 #pragma unroll
@@ -316,38 +332,105 @@ __device__ __forceinline__ void unit_scale(const void* src, void* dst, long long
 #pragma unroll
       for (int k = 0; k < kOut; ++k) __stcs(out + i * kOut + k, D::pack(x + k * D::kVec));
     }
-    for (long long e = e0 + head + nv * kStep + threadIdx.x; e < e1; e += kThreads) D::put(dst, e, S::get(src, e) * s);
+    for (long long e = e0 + head + nv * kStep + tid; e < e1; e += kStride) D::put(dst, e, S::get(src, e) * s);
   }
-  for (long long e = e0 + threadIdx.x; e < e0 + head; e += kThreads) D::put(dst, e, S::get(src, e) * s);
+  for (long long e = e0 + tid; e < e0 + head; e += kStride) D::put(dst, e, S::get(src, e) * s);
 }
 
-template <int kSrc>
-__device__ __forceinline__ void unit_scale_to(int dtype, const void* src, void* dst, long long e0, long long e1,
-                                              int phase, float s) {
-  switch (dtype) {
-    case GRAD_F32: unit_scale<kSrc, GRAD_F32>(src, dst, e0, e1, phase, s); break;
-    case GRAD_BF16: unit_scale<kSrc, GRAD_BF16>(src, dst, e0, e1, phase, s); break;
-    default: unit_scale<kSrc, GRAD_F16>(src, dst, e0, e1, phase, s); break;
+template <int kSrc, int kStride>
+__device__ __forceinline__ void unit_scale_to(unsigned long long meta, const void* src, void* dst, long long e0,
+                                              long long e1, float s, int tid) {
+  const int phase = grad_phase(meta);
+  switch (grad_dst(meta)) {
+    case GRAD_F32: unit_scale<kSrc, GRAD_F32, kStride>(src, dst, e0, e1, phase, s, tid); break;
+    case GRAD_BF16: unit_scale<kSrc, GRAD_BF16, kStride>(src, dst, e0, e1, phase, s, tid); break;
+    default: unit_scale<kSrc, GRAD_F16, kStride>(src, dst, e0, e1, phase, s, tid); break;
+  }
+}
+
+template <int kStride>
+__device__ __forceinline__ void unit_scale(unsigned long long meta, const void* src, void* dst, long long e0,
+                                           long long e1, float s, int tid) {
+  if (s == 1.0f && src == dst) return;   // in place and inside the bound: nothing changes
+  switch (grad_src(meta)) {
+    case GRAD_F32: unit_scale_to<GRAD_F32, kStride>(meta, src, dst, e0, e1, s, tid); break;
+    case GRAD_BF16: unit_scale_to<GRAD_BF16, kStride>(meta, src, dst, e0, e1, s, tid); break;
+    default: unit_scale_to<GRAD_F16, kStride>(meta, src, dst, e0, e1, s, tid); break;
   }
 }
 
 template <int kCap>
 __global__ void __launch_bounds__(kThreads) g3_scale(const __grid_constant__ ScaleTable<kCap> t, int unit,
                                                      const float* __restrict__ scale) {
-  dep_wait();
-  dep_release();
-  const float s = *scale;
   // Last unit first: what the norm's pass read last is still in L2.
   const int blk = (int)(gridDim.x - 1 - blockIdx.x);
   const int i = find_tensor(t.unit0, t.count, blk);
   const unsigned long long meta = t.meta[i];
-  if (s == 1.0f && t.src[i] == t.dst[i]) return;   // in place and inside the bound: nothing changes
   const long long e0 = (long long)(blk - t.unit0[i]) * unit;
   const long long e1 = min(e0 + unit, grad_numel(meta));
-  switch (grad_src(meta)) {
-    case GRAD_F32: unit_scale_to<GRAD_F32>(grad_dst(meta), t.src[i], t.dst[i], e0, e1, grad_phase(meta), s); break;
-    case GRAD_BF16: unit_scale_to<GRAD_BF16>(grad_dst(meta), t.src[i], t.dst[i], e0, e1, grad_phase(meta), s); break;
-    default: unit_scale_to<GRAD_F16>(grad_dst(meta), t.src[i], t.dst[i], e0, e1, grad_phase(meta), s); break;
+  dep_wait();
+  dep_release();
+  unit_scale<kThreads>(meta, t.src[i], t.dst[i], e0, e1, __ldcg(scale), threadIdx.x);
+}
+
+// ---------------------------------------------------------------------------
+// Small lists: norm, and clipped copy, in one kernel on one cluster
+// ---------------------------------------------------------------------------
+
+// A small list costs launches, not bytes: here the cluster's barrier takes the
+// place of the second and third launch. A warp takes a unit of 1024 elements;
+// the partials go through global memory (they stay in L2), and every block
+// adds them all, in the same order, to have the multiplier.
+constexpr int kSmallBlocks = 8;      // the largest portable cluster
+constexpr int kSmallThreads = 1024;
+
+template <class Acc, int kCap, bool kScale>
+__global__ void __cluster_dims__(kSmallBlocks, 1, 1) __launch_bounds__(kSmallThreads)
+    g5_small(const __grid_constant__ ScaleTable<kCap> t, float max_norm, float* __restrict__ out, Acc* partials,
+             float* __restrict__ per_tensor) {
+  __shared__ float shared_scale;
+  const int lane = threadIdx.x & 31;
+  const int warp = (int)(threadIdx.x >> 5) * kSmallBlocks + (int)blockIdx.x;   // over the cluster, blocks in turn
+  constexpr int kWarps = kSmallBlocks * kSmallThreads / 32;
+  const int nunits = t.unit0[t.count];
+  dep_wait();
+  dep_release();
+  for (int u = warp; u < nunits; u += kWarps) {
+    const int i = find_tensor(t.unit0, t.count, u);
+    const unsigned long long meta = t.meta[i];
+    const long long e0 = (long long)(u - t.unit0[i]) * kGradSmallUnit;
+    const long long e1 = min(e0 + kGradSmallUnit, grad_numel(meta));
+    Acc a = unit_norm<Acc, 32>(grad_src(meta), t.src[i], e0, e1, lane);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a.join(a.peer(o));
+    if (lane == 0) partials[u] = a;
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (kScale || blockIdx.x == 0) {
+    const Acc a = join_partials<Acc, kSmallThreads>(partials, nunits);
+    if (threadIdx.x == 0) {
+      const double norm = a.norm();
+      shared_scale = clip_scale(norm, max_norm);
+      if (blockIdx.x == 0) {
+        out[0] = (float)norm;
+        out[1] = shared_scale;
+      }
+    }
+  }
+  if (kScale) {
+    __syncthreads();
+    const float s = shared_scale;
+    for (int u = warp; u < nunits; u += kWarps) {
+      const int i = find_tensor(t.unit0, t.count, u);
+      const unsigned long long meta = t.meta[i];
+      const long long e0 = (long long)(u - t.unit0[i]) * kGradSmallUnit;
+      const long long e1 = min(e0 + kGradSmallUnit, grad_numel(meta));
+      unit_scale<32>(meta, t.src[i], t.dst[i], e0, e1, s, lane);
+    }
+  } else if (per_tensor != nullptr) {
+    for (int i = warp; i < t.count; i += kWarps) tensor_norm(t.unit0, i, partials, per_tensor);
   }
 }
 
@@ -413,34 +496,26 @@ __device__ __forceinline__ void unit_adamw(float* p, const void* g, float* m, fl
 template <int kCap>
 __global__ void __launch_bounds__(kThreads) g4_adamw(const __grid_constant__ AdamTable<kCap> t, int unit,
                                                      const __grid_constant__ AdamArgs a) {
-  dep_wait();
-  dep_release();
-  __shared__ AdamW sh;
-  if (threadIdx.x == 0) {
-    AdamW f;
-    f.decay = a.decay;
-    f.b1 = (float)a.beta1;
-    f.omb1 = (float)(1.0 - a.beta1);
-    f.b2 = (float)a.beta2;
-    f.omb2 = (float)(1.0 - a.beta2);
-    f.eps = a.eps;
-    f.step_size = a.step_size;
-    f.rsqrt_bc2 = a.rsqrt_bc2;
-    if (a.step != nullptr) {
-      const double k = (double)*a.step;
-      f.step_size = (float)(a.lr / (1.0 - pow(a.beta1, k)));
-      f.rsqrt_bc2 = (float)(1.0 / sqrt(1.0 - pow(a.beta2, k)));
-    }
-    f.gscale = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
-    sh = f;
-  }
-  __syncthreads();
-  const AdamW f = sh;
   const int blk = (int)(gridDim.x - 1 - blockIdx.x);   // as g3_scale: what was read last is still in L2
   const int i = find_tensor(t.unit0, t.count, blk);
   const unsigned long long meta = t.meta[i];
   const long long e0 = (long long)(blk - t.unit0[i]) * unit;
   const long long e1 = min(e0 + unit, grad_numel(meta));
+  AdamW f{a.decay, a.b1, a.omb1, a.b2, a.omb2, a.eps, a.step_size, a.rsqrt_bc2, 1.0f};
+  dep_wait();
+  dep_release();
+  if (a.grad_scale != nullptr) f.gscale = __ldcg(a.grad_scale);
+  if (a.step != nullptr) {
+    __shared__ float corr[2];
+    if (threadIdx.x == 0) {
+      const double k = (double)__ldcg(a.step);
+      corr[0] = (float)(a.lr / (1.0 - pow(a.beta1, k)));
+      corr[1] = (float)(1.0 / sqrt(1.0 - pow(a.beta2, k)));
+    }
+    __syncthreads();
+    f.step_size = corr[0];
+    f.rsqrt_bc2 = corr[1];
+  }
   switch (grad_src(meta)) {
     case GRAD_F32: unit_adamw<GRAD_F32>(t.p[i], t.g[i], t.m[i], t.v[i], e0, e1, grad_phase(meta), f); break;
     case GRAD_BF16: unit_adamw<GRAD_BF16>(t.p[i], t.g[i], t.m[i], t.v[i], e0, e1, grad_phase(meta), f); break;
@@ -468,17 +543,35 @@ cudaError_t launch_dep(void (*kernel)(P...), unsigned grid, unsigned block, cuda
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
-// Elements of phase shared by the pointers (esize bytes each element), or kNoPhase.
-int common_phase(const void* const* ptr, const int* esize, int n) {
-  for (int h = 0; h < 8; ++h) {
-    bool ok = true;
-    for (int k = 0; k < n; ++k) ok = ok && (reinterpret_cast<uintptr_t>(ptr[k]) + (uintptr_t)(h * esize[k])) % 16 == 0;
-    if (ok) return h;
+int esize(int type) { return type == GRAD_F32 ? 4 : 2; }
+
+// Elements (0 to 7) after which every pointer is on a 16-byte boundary, or
+// kNoPhase; types[k] is pointer k's element type.
+int common_phase(const void* const* ptr, const int* types, int n) {
+  int h = 0;
+  for (int k = 0; k < n; ++k) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(ptr[k]) / (uintptr_t)esize(types[k]);
+    if (types[k] != GRAD_F32) h = (int)(-at & 7);
+    else if (h < 4 && k == 0) h = (int)(-at & 3);
   }
-  return kNoPhase;
+  for (int k = 0; k < n; ++k)
+    if ((reinterpret_cast<uintptr_t>(ptr[k]) + (uintptr_t)(h * esize(types[k]))) % 16) return kNoPhase;
+  return h;
 }
 
-int esize(int type) { return type == GRAD_F32 ? 4 : 2; }
+template <int kCap>
+void fill(ScaleTable<kCap>& t, const GradItem* it, int n, int unit) {
+  t.count = n;
+  t.unit0[0] = 0;
+  for (int i = 0; i < n; ++i) {
+    t.src[i] = it[i].src;
+    t.dst[i] = it[i].dst;
+    const void* ptr[2] = {it[i].src, it[i].dst};
+    const int types[2] = {it[i].stype, it[i].dtype};
+    t.meta[i] = grad_meta(it[i].numel, it[i].stype, it[i].dtype, common_phase(ptr, types, 2));
+    t.unit0[i + 1] = t.unit0[i] + grad_units(it[i].numel, unit);
+  }
+}
 
 template <class Acc, int kCap>
 cudaError_t norm_launch(const GradItem* it, int n, int unit, int units, double* partials, cudaStream_t st) {
@@ -493,20 +586,32 @@ cudaError_t norm_launch(const GradItem* it, int n, int unit, int units, double* 
   return launch_dep(g1_norm<Acc, kCap>, (unsigned)units, kThreads, st, t, unit, reinterpret_cast<Acc*>(partials));
 }
 
+template <class Acc, int kCap>
+cudaError_t finish_launch(const GradItem* it, int n, int unit, const double* all, long long nunits, float max_norm,
+                          float* out, const double* partials, float* per_tensor, cudaStream_t st) {
+  SpanTable<kCap> t;
+  t.count = n;
+  t.unit0[0] = 0;
+  for (int i = 0; i < n; ++i) t.unit0[i + 1] = t.unit0[i] + grad_units(it[i].numel, unit);
+  const unsigned grid = 1 + (unsigned)((n + kFinishThreads / 32 - 1) / (kFinishThreads / 32));
+  return launch_dep(g2_finish<Acc, kCap>, grid, kFinishThreads, st, t, reinterpret_cast<const Acc*>(all), nunits,
+                    max_norm, out, reinterpret_cast<const Acc*>(partials), per_tensor);
+}
+
 template <int kCap>
 cudaError_t scale_launch(const GradItem* it, int n, int unit, int units, const float* scale, cudaStream_t st) {
   ScaleTable<kCap> t;
-  t.count = n;
-  t.unit0[0] = 0;
-  for (int i = 0; i < n; ++i) {
-    t.src[i] = it[i].src;
-    t.dst[i] = it[i].dst;
-    const void* ptr[2] = {it[i].src, it[i].dst};
-    const int es[2] = {esize(it[i].stype), esize(it[i].dtype)};
-    t.meta[i] = grad_meta(it[i].numel, it[i].stype, it[i].dtype, common_phase(ptr, es, 2));
-    t.unit0[i + 1] = t.unit0[i] + grad_units(it[i].numel, unit);
-  }
+  fill(t, it, n, unit);
   return launch_dep(g3_scale<kCap>, (unsigned)units, kThreads, st, t, unit, scale);
+}
+
+template <class Acc, int kCap>
+cudaError_t small_launch(const GradItem* it, int n, bool scale, float max_norm, float* out, float* per_tensor,
+                         double* partials, cudaStream_t st) {
+  ScaleTable<kCap> t;
+  fill(t, it, n, kGradSmallUnit);
+  return launch_dep(scale ? g5_small<Acc, kCap, true> : g5_small<Acc, kCap, false>, kSmallBlocks, kSmallThreads, st, t,
+                    max_norm, out, reinterpret_cast<Acc*>(partials), per_tensor);
 }
 
 template <int kCap>
@@ -519,51 +624,70 @@ cudaError_t adamw_launch(const AdamItem* it, int n, int unit, int units, const A
     t.g[i] = it[i].g;
     t.m[i] = it[i].m;
     t.v[i] = it[i].v;
-    const void* ptr[4] = {it[i].p, it[i].g, it[i].m, it[i].v};
-    const int es[4] = {4, esize(it[i].gtype), 4, 4};
-    t.meta[i] = grad_meta(it[i].numel, it[i].gtype, GRAD_F32, common_phase(ptr, es, 4));
+    const void* ptr[4] = {it[i].p, it[i].m, it[i].v, it[i].g};
+    const int types[4] = {GRAD_F32, GRAD_F32, GRAD_F32, it[i].gtype};
+    t.meta[i] = grad_meta(it[i].numel, it[i].gtype, GRAD_F32, common_phase(ptr, types, 4));
     t.unit0[i + 1] = t.unit0[i] + grad_units(it[i].numel, unit);
   }
   return launch_dep(g4_adamw<kCap>, (unsigned)units, kThreads, st, t, unit, a);
+}
+
+template <class Acc>
+cudaError_t norm_for(const GradItem* it, int n, int unit, int units, double* partials, cudaStream_t st) {
+  if (n <= kGradCapSmall) return norm_launch<Acc, kGradCapSmall>(it, n, unit, units, partials, st);
+  if (n <= kGradCapMid) return norm_launch<Acc, kGradCapMid>(it, n, unit, units, partials, st);
+  return norm_launch<Acc, kNormCap>(it, n, unit, units, partials, st);
+}
+
+template <class Acc>
+cudaError_t finish_for(const GradItem* it, int n, int unit, const double* all, long long nunits, float max_norm,
+                       float* out, const double* partials, float* per_tensor, cudaStream_t st) {
+  if (!per_tensor) n = 0;
+  if (n <= kGradCapSmall)
+    return finish_launch<Acc, kGradCapSmall>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st);
+  return finish_launch<Acc, kNormCap>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st);
+}
+
+template <class Acc>
+cudaError_t small_for(const GradItem* it, int n, bool scale, float max_norm, float* out, float* per_tensor,
+                      double* partials, cudaStream_t st) {
+  if (n <= kGradCapSmall)
+    return small_launch<Acc, kGradCapSmall>(it, n, scale, max_norm, out, per_tensor, partials, st);
+  return small_launch<Acc, kGradCapMid>(it, n, scale, max_norm, out, per_tensor, partials, st);
 }
 
 }  // namespace
 
 cudaError_t launch_grad_norm(const GradItem* it, int n, int unit, int units, int kind, double* partials,
                              cudaStream_t st) {
-  if (units <= 0) return cudaSuccess;
-  if (kind == GRAD_NORM_INF)
-    return n <= kGradCapSmall ? norm_launch<MaxAbs, kGradCapSmall>(it, n, unit, units, partials, st)
-                              : norm_launch<MaxAbs, kNormCap>(it, n, unit, units, partials, st);
-  return n <= kGradCapSmall ? norm_launch<SumSq, kGradCapSmall>(it, n, unit, units, partials, st)
-                            : norm_launch<SumSq, kNormCap>(it, n, unit, units, partials, st);
+  return kind == GRAD_NORM_INF ? norm_for<MaxAbs>(it, n, unit, units, partials, st)
+                               : norm_for<SumSq>(it, n, unit, units, partials, st);
 }
 
 cudaError_t launch_grad_finish(const GradItem* it, int n, int unit, int kind, const double* all, long long nunits,
                                float max_norm, float* out, const double* partials, float* per_tensor,
                                cudaStream_t st) {
-  SpanTable t;
-  t.count = per_tensor ? n : 0;
-  t.unit0[0] = 0;
-  for (int i = 0; i < t.count; ++i) t.unit0[i + 1] = t.unit0[i] + grad_units(it[i].numel, unit);
-  const unsigned grid = 1 + (unsigned)((t.count + kFinishThreads / 32 - 1) / (kFinishThreads / 32));
-  if (kind == GRAD_NORM_INF)
-    return launch_dep(g2_finish<MaxAbs>, grid, kFinishThreads, st, t, reinterpret_cast<const MaxAbs*>(all), nunits,
-                      max_norm, out, reinterpret_cast<const MaxAbs*>(partials), per_tensor);
-  return launch_dep(g2_finish<SumSq>, grid, kFinishThreads, st, t, reinterpret_cast<const SumSq*>(all), nunits,
-                    max_norm, out, reinterpret_cast<const SumSq*>(partials), per_tensor);
+  return kind == GRAD_NORM_INF
+             ? finish_for<MaxAbs>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st)
+             : finish_for<SumSq>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st);
+}
+
+cudaError_t launch_grad_small(const GradItem* it, int n, int kind, bool scale, float max_norm, float* out,
+                              float* per_tensor, double* partials, cudaStream_t st) {
+  return kind == GRAD_NORM_INF ? small_for<MaxAbs>(it, n, scale, max_norm, out, per_tensor, partials, st)
+                               : small_for<SumSq>(it, n, scale, max_norm, out, per_tensor, partials, st);
 }
 
 cudaError_t launch_grad_scale(const GradItem* it, int n, int unit, int units, const float* scale, cudaStream_t st) {
-  if (units <= 0) return cudaSuccess;
-  return n <= kGradCapSmall ? scale_launch<kGradCapSmall>(it, n, unit, units, scale, st)
-                            : scale_launch<kScaleCap>(it, n, unit, units, scale, st);
+  if (n <= kGradCapSmall) return scale_launch<kGradCapSmall>(it, n, unit, units, scale, st);
+  if (n <= kGradCapMid) return scale_launch<kGradCapMid>(it, n, unit, units, scale, st);
+  return scale_launch<kScaleCap>(it, n, unit, units, scale, st);
 }
 
 cudaError_t launch_adamw(const AdamItem* it, int n, int unit, int units, const AdamArgs& a, cudaStream_t st) {
-  if (units <= 0) return cudaSuccess;
-  return n <= kGradCapSmall ? adamw_launch<kGradCapSmall>(it, n, unit, units, a, st)
-                            : adamw_launch<kAdamCap>(it, n, unit, units, a, st);
+  if (n <= kGradCapSmall) return adamw_launch<kGradCapSmall>(it, n, unit, units, a, st);
+  if (n <= kGradCapMid) return adamw_launch<kGradCapMid>(it, n, unit, units, a, st);
+  return adamw_launch<kAdamCap>(it, n, unit, units, a, st);
 }
 
 }  // namespace muon

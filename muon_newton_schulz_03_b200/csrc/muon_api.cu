@@ -1202,23 +1202,58 @@ int check_elem_ptr(const void* p, size_t esize, const char* what, int i) {
 }
 
 // Memory ranges of a call: no written one may meet any other.
-struct Ranges {
-  struct R { uintptr_t a, b; bool written; };
-  std::vector<R> r;
+class Ranges {
+ public:
+  explicit Ranges(size_t n) { r_.reserve(n); }
   void add(const void* p, size_t bytes, bool written) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    if (bytes) r.push_back({a, a + bytes, written});
+    if (bytes) r_.push_back({a, (bytes << 1) | (written ? 1 : 0)});
   }
   bool clash() {
-    std::sort(r.begin(), r.end(), [](const R& x, const R& y) { return x.a < y.a; });
+    sort();
     uintptr_t any = 0, written = 0;
-    for (const R& x : r) {
-      if (x.a < written || (x.written && x.a < any)) return true;
-      any = std::max(any, x.b);
-      if (x.written) written = std::max(written, x.b);
+    for (const R& x : r_) {
+      const uintptr_t end = x.a + (x.len >> 1);
+      const bool w = x.len & 1;
+      if (x.a < written || (w && x.a < any)) return true;
+      any = std::max(any, end);
+      if (w) written = std::max(written, end);
     }
     return false;
   }
+
+ private:
+  struct R {
+    uintptr_t a;
+    size_t len;   // bytes << 1 | written
+  };
+  // By address: dealt into about as many buckets as ranges, then each bucket
+  // (a handful, whatever the lists' order) on its own.
+  void sort() {
+    const auto less = [](const R& x, const R& y) { return x.a < y.a; };
+    if (std::is_sorted(r_.begin(), r_.end(), less)) return;
+    if (r_.size() < 32) {
+      std::sort(r_.begin(), r_.end(), less);
+      return;
+    }
+    uintptr_t lo = r_[0].a, hi = lo;
+    for (const R& x : r_) {
+      lo = std::min(lo, x.a);
+      hi = std::max(hi, x.a);
+    }
+    int shift = 0;
+    while (((hi - lo) >> shift) >= 2 * r_.size()) ++shift;
+    std::vector<uint32_t> at(((hi - lo) >> shift) + 2, 0);
+    for (const R& x : r_) ++at[((x.a - lo) >> shift) + 1];
+    for (size_t k = 1; k < at.size(); ++k) at[k] += at[k - 1];
+    std::vector<R> out(r_.size());
+    std::vector<uint32_t> next(at.begin(), at.end() - 1);
+    for (const R& x : r_) out[next[(x.a - lo) >> shift]++] = x;
+    for (size_t k = 0; k + 1 < at.size(); ++k)
+      if (at[k + 1] - at[k] > 1) std::sort(out.begin() + at[k], out.begin() + at[k + 1], less);
+    r_.swap(out);
+  }
+  std::vector<R> r_;
 };
 
 // Elements a block takes: about `units` blocks for the list, at least `least`
@@ -1234,10 +1269,25 @@ long long count_units(const std::vector<GradItem>& it, int unit) {
   return u;
 }
 
+// Whether a list takes the one-kernel form.
+bool grad_is_small(const std::vector<GradItem>& it, long long total) {
+  return (int)it.size() <= kGradCapMid && total <= kGradSmallNumel;
+}
+
+int enqueue_grad_small(muon_handle* h, const std::vector<GradItem>& it, int kind, bool scale, float max_norm,
+                       float* out, float* per_tensor, double* partials, cudaStream_t st, int* launches) {
+  const int slot = prof_before(h, MUON_KERNEL_GRAD_SMALL, st);
+  MUON_CUDA_TRY(launch_grad_small(it.data(), (int)it.size(), kind, scale, max_norm, out, per_tensor, partials, st));
+  prof_after(h, slot, st);
+  ++*launches;
+  return MUON_OK;
+}
+
 // Norm of the list into out (norm, multiplier) and per_tensor; the caller has
 // checked everything.
 int enqueue_grad_norm(muon_handle* h, const std::vector<GradItem>& it, long long total, int kind, float max_norm,
                       float* out, float* per_tensor, double* partials, cudaStream_t st, int* launches) {
+  if (grad_is_small(it, total)) return enqueue_grad_small(h, it, kind, false, max_norm, out, per_tensor, partials, st, launches);
   const int unit = pick_unit(total, kGradUnits, 8192);
   const long long nunits = count_units(it, unit);
   const int count = (int)it.size();
@@ -1489,7 +1539,7 @@ int muon_clip_grads(muon_handle* h, const void* const* src, void* const* dst, co
   if (count > 0 && (!src || !dst)) return fail(MUON_ERR_INVALID_ARG, "src and dst are required");
   if ((rc = check_norm_args(norm_kind, max_norm, out, scratch, scratch_bytes, count))) return rc;
   std::vector<GradItem> it((size_t)count);
-  Ranges ranges;
+  Ranges ranges(2 * (size_t)count);
   for (int i = 0; i < count; ++i) {
     const bool skip = src[i] == nullptr || numels[i] == 0;
     if (!skip) {
@@ -1509,9 +1559,13 @@ int muon_clip_grads(muon_handle* h, const void* const* src, void* const* dst, co
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   prof_call_begin(h);
   int launches = 0;
-  if ((rc = enqueue_grad_norm(h, it, total, norm_kind, max_norm, out, nullptr, static_cast<double*>(scratch), st,
-                              &launches)))
+  double* partials = static_cast<double*>(scratch);
+  if (grad_is_small(it, total)) {
+    rc = enqueue_grad_small(h, it, norm_kind, true, max_norm, out, nullptr, partials, st, &launches);
+    h->last_launches = launches;
     return rc;
+  }
+  if ((rc = enqueue_grad_norm(h, it, total, norm_kind, max_norm, out, nullptr, partials, st, &launches))) return rc;
   const int unit = pick_unit(total, 65536, 4096);
   // Last tensors first, for what is still in L2 (see g3_scale).
   for (int i1 = count; i1 > 0; i1 -= kScaleCap) {
@@ -1547,7 +1601,7 @@ int muon_adamw_step(muon_handle* h, float* const* params, const void* const* gra
   if (reinterpret_cast<uintptr_t>(grad_scale) % 4) return fail(MUON_ERR_INVALID_ARG, "grad_scale is misaligned");
   std::vector<AdamItem> it;
   it.reserve((size_t)count);
-  Ranges ranges;
+  Ranges ranges(4 * (size_t)count);
   for (int i = 0; i < count; ++i) {
     if (grads[i] == nullptr || numels[i] == 0) continue;
     const size_t gs = dtype_size(grad_dtypes[i]), n = (size_t)numels[i];
@@ -1573,6 +1627,10 @@ int muon_adamw_step(muon_handle* h, float* const* params, const void* const* gra
   a.decay = (float)(1.0 - lr * wd);
   a.eps = (float)eps;
   a.step = reinterpret_cast<const long long*>(step_dev);
+  a.b1 = (float)beta1;
+  a.omb1 = (float)(1.0 - beta1);
+  a.b2 = (float)beta2;
+  a.omb2 = (float)(1.0 - beta2);
   a.step_size = a.rsqrt_bc2 = 0.0f;
   if (!step_dev) {
     a.step_size = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
