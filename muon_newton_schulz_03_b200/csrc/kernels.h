@@ -161,12 +161,15 @@ int ns_bf16_smem_bytes();
 enum GradType : int { GRAD_F32 = 0, GRAD_BF16 = 1, GRAD_F16 = 2 };   // muon_dtype
 enum GradNorm : int { GRAD_NORM_L2 = 0, GRAD_NORM_INF = 1 };         // muon_norm_kind
 
-// One tensor of a list: numel = 0 for a skipped one.
+// One tensor of a list: numel = 0 for a skipped one. The phase is the number
+// of elements after which every pointer is on the boundary of the kernels'
+// accesses, kNoPhase if there is none.
 struct GradItem {
   const void* src;
   void* dst;          // clipped copy only
   long long numel;
   int stype, dtype;
+  int norm_phase, scale_phase;   // of src alone; of src and dst
 };
 struct AdamItem {
   float* p;
@@ -175,23 +178,44 @@ struct AdamItem {
   float* v;
   long long numel;
   int gtype;
+  int phase;
 };
+constexpr int kNoPhase = 31;
+// Elements that a thread takes at once: 32 bytes of the wider type.
+constexpr int kAdamStep = 8;
+__host__ __device__ constexpr int norm_step(int src) { return src == GRAD_F32 ? 8 : 16; }
+__host__ __device__ constexpr int scale_step(int src, int dst) { return src == GRAD_F32 || dst == GRAD_F32 ? 8 : 16; }
+// Elements from p to a boundary of `step` elements.
+inline int phase_of(const void* p, int type, int step) {
+  return (int)(-(reinterpret_cast<uintptr_t>(p) >> (type == GRAD_F32 ? 2 : 1)) & (uintptr_t)(step - 1));
+}
+inline void set_phases(GradItem& x) {
+  const int step = scale_step(x.stype, x.dtype), h = phase_of(x.src, x.stype, step);
+  x.norm_phase = phase_of(x.src, x.stype, norm_step(x.stype));
+  x.scale_phase = phase_of(x.dst, x.dtype, step) == h ? h : kNoPhase;
+}
+inline void set_phases(AdamItem& x) {
+  const int h = phase_of(x.p, GRAD_F32, kAdamStep);
+  x.phase = phase_of(x.m, GRAD_F32, kAdamStep) == h && phase_of(x.v, GRAD_F32, kAdamStep) == h &&
+                    phase_of(x.g, x.gtype, kAdamStep) == h
+                ? h
+                : kNoPhase;
+}
 
 // Tables that travel as kernel arguments (at most 32,764 bytes of them). A
 // launch takes the smallest table that the list fits: 31 KB of arguments cost
 // the host 2.2 us more than 3 KB, 11 KB 1.1 us.
 constexpr int kGradCapSmall = 64;
 constexpr int kGradCapMid = 256;
-constexpr int kNormCap = 1536;    // 20 bytes a tensor
+constexpr int kNormCap = 1536;    // 20 bytes a tensor, and 0.5 KB of index
 constexpr int kScaleCap = 1088;   // 28
 constexpr int kAdamCap = 704;     // 44
-constexpr int kNoPhase = 15;
 constexpr int kGradUnits = 32768; // at most this many blocks, and one more per tensor, share a norm
 // Lists up to this size take one kernel on one cluster (launch_grad_small).
 constexpr long long kGradSmallNumel = 1 << 18;
 constexpr int kGradSmallUnit = 1024;   // elements a warp takes there
 
-// numel (48 bits) | source type | destination type | phase
+// numel (48 bits) | source type (2) | destination type (2) | phase (5)
 __host__ __device__ inline unsigned long long grad_meta(long long numel, int stype, int dtype, int phase) {
   return (unsigned long long)numel | ((unsigned long long)stype << 48) | ((unsigned long long)dtype << 50) |
          ((unsigned long long)phase << 52);
@@ -199,23 +223,56 @@ __host__ __device__ inline unsigned long long grad_meta(long long numel, int sty
 __host__ __device__ inline long long grad_numel(unsigned long long m) { return (long long)(m & 0xffffffffffffull); }
 __host__ __device__ inline int grad_src(unsigned long long m) { return (int)(m >> 48) & 3; }
 __host__ __device__ inline int grad_dst(unsigned long long m) { return (int)(m >> 50) & 3; }
-__host__ __device__ inline int grad_phase(unsigned long long m) { return (int)(m >> 52) & 15; }
-__host__ __device__ inline int grad_units(long long numel, int unit) { return (int)((numel + unit - 1) / unit); }
+__host__ __device__ inline int grad_phase(unsigned long long m) { return (int)(m >> 52) & 31; }
+// Units of a tensor. They are counted from its phase (the first one takes the
+// elements before it too), so that only a tensor's first and last unit have
+// elements outside the wide accesses: a second pass of a block over a few
+// elements costs as much time as its first.
+__host__ __device__ inline int grad_units(long long numel, int phase, int unit) {
+  if (numel == 0) return 0;
+  const long long rest = numel - (phase == kNoPhase ? 0 : phase);
+  return rest <= unit ? 1 : (int)((rest + unit - 1) / unit);
+}
+struct UnitRange {
+  long long e0, e1;   // elements
+  int head;           // the first ones, before the boundary; all of them without a phase
+};
+__host__ __device__ inline UnitRange unit_range(unsigned long long meta, int k, int unit) {
+  const int phase = grad_phase(meta);
+  const long long numel = grad_numel(meta), first = phase == kNoPhase ? 0 : phase;
+  UnitRange r;
+  r.e0 = k == 0 ? 0 : first + (long long)k * unit;
+  r.e1 = first + (long long)(k + 1) * unit;
+  if (r.e1 > numel) r.e1 = numel;
+  const int n = (int)(r.e1 - r.e0);
+  r.head = phase == kNoPhase ? n : k > 0 ? 0 : phase < n ? phase : n;
+  return r;
+}
 
+// Where every tensor's units begin, and where to look for a unit's tensor: the
+// units fall into at most kBuckets buckets of 2^shift, and tensor_of[k] holds
+// the first unit of bucket k. A block then finds its tensor in two or three
+// dependent reads of its arguments instead of a search over the whole list.
+constexpr int kBuckets = 256;
+template <int kCap>
+struct UnitIndex {
+  int unit0[kCap + 1];
+  unsigned short tensor_of[kBuckets + 1];
+  unsigned short count;
+  int shift;
+};
 template <int kCap>
 struct GradTable {
   const void* src[kCap];
   unsigned long long meta[kCap];
-  int unit0[kCap + 1];
-  int count;
+  UnitIndex<kCap> units;
 };
 template <int kCap>
 struct ScaleTable {
   const void* src[kCap];
   void* dst[kCap];
   unsigned long long meta[kCap];
-  int unit0[kCap + 1];
-  int count;
+  UnitIndex<kCap> units;
 };
 template <int kCap>
 struct AdamTable {
@@ -224,8 +281,7 @@ struct AdamTable {
   float* m[kCap];
   float* v[kCap];
   unsigned long long meta[kCap];
-  int unit0[kCap + 1];
-  int count;
+  UnitIndex<kCap> units;
 };
 template <int kCap>
 struct SpanTable {

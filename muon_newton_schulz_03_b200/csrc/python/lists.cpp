@@ -44,22 +44,45 @@ int type_of(const at::Tensor& t) {
   }
 }
 
-// A dense strided tensor of an allowed type on the device, laid out like `like`.
-bool take(PyObject* o, int64_t device, int allowed, const at::Tensor* like, Column& c, size_t i) {
+// Whether a tensor is strided memory on a CUDA device, read as it is. That
+// follows from its set of dispatch keys, so it is asked once per set: nearly
+// all tensors of a program have the same one.
+bool is_plain(const at::Tensor& t) {
+  static thread_local uint64_t known = 0;
+  const uint64_t keys = t.unsafeGetTensorImpl()->key_set().raw_repr();
+  if (keys == known) return true;
+  if (t.layout() != at::kStrided || !t.is_cuda() || t.is_neg()) return false;
+  known = keys;
+  return true;
+}
+
+// What the entries of one row have in common.
+struct Row {
+  c10::IntArrayRef sizes, strides;
+  bool contiguous;
+};
+
+// A dense strided tensor of an allowed type on the device; `first`: of its
+// row, whose others are laid out like it.
+bool take(PyObject* o, c10::Device device, int allowed, bool first, Row& row, Column& c, size_t i) {
   if (!THPVariable_Check(o)) return false;
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (t.layout() != at::kStrided || !t.is_cuda() || t.get_device() != device || t.is_neg()) return false;
+  if (!is_plain(t)) return false;
+  const c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+  if (impl->device() != device) return false;
   const int type = type_of(t);
   if (type < 0 || !((allowed >> type) & 1)) return false;
-  const bool contiguous = t.is_contiguous();
-  if (!contiguous && !t.unsafeGetTensorImpl()->is_non_overlapping_and_dense()) return false;
-  if (like != nullptr) {
-    if (t.sizes() != like->sizes()) return false;
-    if (!(contiguous && like->is_contiguous()) && t.strides() != like->strides()) return false;
+  const bool contiguous = impl->is_contiguous();
+  if (!contiguous && !impl->is_non_overlapping_and_dense()) return false;
+  if (first) {
+    row = Row{impl->sizes(), impl->strides(), contiguous};
+  } else {
+    if (impl->sizes() != row.sizes) return false;
+    if (!(contiguous && row.contiguous) && impl->strides() != row.strides) return false;
   }
   c.ptr[i] = t.data_ptr();
   c.type[i] = type;
-  return c.ptr[i] != nullptr || t.numel() == 0;
+  return c.ptr[i] != nullptr || impl->numel() == 0;
 }
 
 // Paired lists; where the first holds None, the entry is skipped.
@@ -72,7 +95,8 @@ struct Lists {
   ~Lists() {
     for (PyObject* s : seq) Py_XDECREF(s);
   }
-  bool read(PyObject* const* lists, const int* allowed, int count, int64_t device) {
+  bool read(PyObject* const* lists, const int* allowed, int count, int64_t device_index) {
+    const c10::Device device(at::kCUDA, (c10::DeviceIndex)device_index);
     for (int k = 0; k < count; ++k) {
       seq[k] = PySequence_Fast(lists[k], "a list of tensors is needed");
       if (!seq[k]) {
@@ -89,11 +113,11 @@ struct Lists {
     for (int i = 0; i < n; ++i) {
       PyObject* o = PySequence_Fast_GET_ITEM(seq[0], i);
       if (o == Py_None) continue;
-      if (!take(o, device, allowed[0], nullptr, col[0], (size_t)i)) return false;
-      const at::Tensor& t = THPVariable_Unpack(o);
-      numel[i] = t.numel();
+      Row row;
+      if (!take(o, device, allowed[0], true, row, col[0], (size_t)i)) return false;
+      numel[i] = THPVariable_Unpack(o).numel();
       for (int k = 1; k < count; ++k)
-        if (!take(PySequence_Fast_GET_ITEM(seq[k], i), device, allowed[k], &t, col[k], (size_t)i)) return false;
+        if (!take(PySequence_Fast_GET_ITEM(seq[k], i), device, allowed[k], false, row, col[k], (size_t)i)) return false;
     }
     return true;
   }
@@ -123,6 +147,7 @@ struct Buffers {
   at::Tensor out, per, scratch;
   size_t bytes;
   Buffers(int64_t device, int n, bool per_tensor) {
+    at::AutoDispatchBelowADInplaceOrView guard;   // plain tensors: nothing to record
     const auto on = at::TensorOptions().device(at::kCUDA, (c10::DeviceIndex)device);
     bytes = MUON_GRAD_SCRATCH_BYTES(n);
     out = at::empty({2}, on.dtype(at::kFloat));
