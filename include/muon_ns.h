@@ -271,7 +271,7 @@ enum muon_norm_kind {
 };
 
 /* Bytes of device scratch for a list of `count` tensors. */
-#define MUON_GRAD_SCRATCH_BYTES(count) ((size_t)8 * ((size_t)32768 + (size_t)(count)))
+#define MUON_GRAD_SCRATCH_BYTES(count) ((size_t)8 * ((size_t)65536 + (size_t)(count)))
 
 /* Norm of all tensors together and its clip multiplier.
  *   tensors    : device pointers; NULL skips tensor i (it adds nothing).

@@ -212,9 +212,10 @@ def _bad_lists(device, lists):
 
 def _check_scalar(t, what, dtype, device):
     """A one-element CUDA tensor, or None."""
+    import torch
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != 1:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != 1:
         raise ValueError(f"{what} must be a {dtype} tensor of one element")
     if t.device.type != "cuda" or t.device.index != device:
         raise ValueError(f"{what} must be on cuda:{device}, got {t.device}")
@@ -479,18 +480,18 @@ class Muon:
         if stream is not None:
             with self._on(stream):
                 return self.adamw_step(params, grads, exp_avgs, exp_avg_sqs, lr, step, betas, eps, wd, grad_scale)
-        import torch
-        lists = [_sequence(ts) for ts in (grads, params, exp_avgs, exp_avg_sqs)]
-        at = 0
-        if isinstance(step, torch.Tensor):
-            step, at = 0, _check_scalar(step, "step", torch.int64, self.device)
-        r = self._lists.adamw_step(self._hv, self.device, *lists, lr, betas[0], betas[1], eps, wd, step, at,
-                                   _check_scalar(grad_scale, "grad_scale", torch.float32, self.device) or 0)
+        lists = (_sequence(grads), _sequence(params), _sequence(exp_avgs), _sequence(exp_avg_sqs))
+        r = self._lists.adamw_step(self._hv, self.device, *lists, lr, betas[0], betas[1], eps, wd, step, grad_scale)
         if r is None:
+            import torch
+            if isinstance(step, torch.Tensor):
+                _check_scalar(step, "step", torch.int64, self.device)
+            _check_scalar(grad_scale, "grad_scale", torch.float32, self.device)
             f32 = (torch.float32,)
             _bad_lists(self.device, [("grads", lists[0], _grad_dtypes()), ("params", lists[1], f32),
                                      ("exp_avgs", lists[2], f32), ("exp_avg_sqs", lists[3], f32)])
-        check(r)
+        if r:
+            check(r)
 
     def qk_clip(self, weights, s_max, head_rows, tau=100.0, stream=None):
         """QK-Clip in place on W_q / W_k weights (fp32 CUDA tensors).

@@ -210,10 +210,10 @@ constexpr int kGradCapMid = 256;
 constexpr int kNormCap = 1536;    // 20 bytes a tensor, and 0.5 KB of index
 constexpr int kScaleCap = 1088;   // 28
 constexpr int kAdamCap = 704;     // 44
-constexpr int kGradUnits = 32768; // at most this many blocks, and one more per tensor, share a norm
+constexpr int kGradUnits = 65536; // at most this many blocks, and one more per tensor, share a norm
 // Lists up to this size take one kernel on one cluster (launch_grad_small).
-constexpr long long kGradSmallNumel = 1 << 18;
-constexpr int kGradSmallUnit = 1024;   // elements a warp takes there
+constexpr long long kGradSmallNumel = 1 << 17;
+constexpr int kGradSmallUnit = 10;   // log2 of the elements a warp takes there
 
 // numel (48 bits) | source type (2) | destination type (2) | phase (5)
 __host__ __device__ inline unsigned long long grad_meta(long long numel, int stype, int dtype, int phase) {
@@ -228,21 +228,21 @@ __host__ __device__ inline int grad_phase(unsigned long long m) { return (int)(m
 // elements before it too), so that only a tensor's first and last unit have
 // elements outside the wide accesses: a second pass of a block over a few
 // elements costs as much time as its first.
-__host__ __device__ inline int grad_units(long long numel, int phase, int unit) {
+__host__ __device__ inline int grad_units(long long numel, int phase, int log2_unit) {
   if (numel == 0) return 0;
-  const long long rest = numel - (phase == kNoPhase ? 0 : phase);
-  return rest <= unit ? 1 : (int)((rest + unit - 1) / unit);
+  const long long rest = numel - (phase == kNoPhase ? 0 : phase), unit = 1ll << log2_unit;
+  return rest <= unit ? 1 : (int)((rest + unit - 1) >> log2_unit);
 }
 struct UnitRange {
   long long e0, e1;   // elements
   int head;           // the first ones, before the boundary; all of them without a phase
 };
-__host__ __device__ inline UnitRange unit_range(unsigned long long meta, int k, int unit) {
+__host__ __device__ inline UnitRange unit_range(unsigned long long meta, int k, int log2_unit) {
   const int phase = grad_phase(meta);
   const long long numel = grad_numel(meta), first = phase == kNoPhase ? 0 : phase;
   UnitRange r;
-  r.e0 = k == 0 ? 0 : first + (long long)k * unit;
-  r.e1 = first + (long long)(k + 1) * unit;
+  r.e0 = k == 0 ? 0 : first + ((long long)k << log2_unit);
+  r.e1 = first + ((long long)(k + 1) << log2_unit);
   if (r.e1 > numel) r.e1 = numel;
   const int n = (int)(r.e1 - r.e0);
   r.head = phase == kNoPhase ? n : k > 0 ? 0 : phase < n ? phase : n;
@@ -298,22 +298,22 @@ struct AdamArgs {
   const float* grad_scale;          // device multiplier of the gradients, or NULL
 };
 
-// Each launches one kernel over up to the table's capacity of tensors.
-// Partial k of the launch is the norm of its unit k; `units` is their number.
-cudaError_t launch_grad_norm(const GradItem* it, int n, int unit, int units, int kind, double* partials,
-                             cudaStream_t st);
+// Each launches one kernel over up to the table's capacity of tensors, in
+// units of 2^unit elements; *units receives their number (0: no launch).
+// Partial k of the launch is the norm of its unit k.
+cudaError_t launch_grad_norm(const GradItem* it, int n, int unit, int kind, double* partials, cudaStream_t st,
+                             int* units);
 // out (or NULL): norm and clip multiplier over all `nunits` partials at `all`.
 // per_tensor (or NULL): norms of these n tensors, whose partials start at `partials`.
 cudaError_t launch_grad_finish(const GradItem* it, int n, int unit, int kind, const double* all, long long nunits,
                                float max_norm, float* out, const double* partials, float* per_tensor,
                                cudaStream_t st);
 // Both of the above, and with `scale` the clipped copy too, in one kernel:
-// lists of up to kGradCapMid tensors and kGradSmallNumel elements. partials
-// holds one entry per kGradSmallUnit elements and one per tensor.
+// lists of up to kGradCapMid tensors and kGradSmallNumel elements.
 cudaError_t launch_grad_small(const GradItem* it, int n, int kind, bool scale, float max_norm, float* out,
-                              float* per_tensor, double* partials, cudaStream_t st);
-cudaError_t launch_grad_scale(const GradItem* it, int n, int unit, int units, const float* scale, cudaStream_t st);
-cudaError_t launch_adamw(const AdamItem* it, int n, int unit, int units, const AdamArgs& a, cudaStream_t st);
+                              float* per_tensor, cudaStream_t st);
+cudaError_t launch_grad_scale(const GradItem* it, int n, int unit, const float* scale, cudaStream_t st, int* units);
+cudaError_t launch_adamw(const AdamItem* it, int n, int unit, const AdamArgs& a, cudaStream_t st);
 
 // Sets the calling thread's muon_last_error text.
 void record_last_error(const std::string& msg);

@@ -1195,88 +1195,74 @@ int check_list(const int64_t* numels, const int32_t* dtypes, int count, const ch
   return MUON_OK;
 }
 
-inline bool good_elem_ptr(const void* p, size_t esize) {
-  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (esize - 1)) == 0;
+inline int check_elem_ptr(const void* p, size_t esize, const char* what, int i) {
+  if (p != nullptr && (reinterpret_cast<uintptr_t>(p) & (esize - 1)) == 0) return MUON_OK;
+  return bad_tensor(what, i, p == nullptr ? "is NULL" : "is not aligned to its element size");
 }
 
-int check_elem_ptr(const void* p, size_t esize, const char* what, int i) {
-  if (p == nullptr) return bad_tensor(what, i, "is NULL");
-  if (!good_elem_ptr(p, esize)) return bad_tensor(what, i, "is not aligned to its element size");
-  return MUON_OK;
-}
-
-// Memory ranges of a call: no written one may meet any other.
+// Whether, of a call's memory ranges, a written one meets any other. each(emit)
+// calls emit(pointer, bytes, written) for every range.
 //
-// Ranges mostly come in a few ascending runs (tensors cut from flat buffers,
-// or allocated one after another), and then it is enough that no two runs
-// meet. Else they are sorted (1600 ranges: 13 us, several kernels' launches).
-class Ranges {
- public:
-  explicit Ranges(size_t n) { r_.reserve(n); }
-  void add(const void* p, size_t bytes, bool written) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = a + bytes;
-    if (!bytes) return;
-    r_.push_back({a, b, written});
-    // Behind a run that ends a little before it; the runs take turns, as the
-    // lists do.
-    for (int k = 0; k < nruns_; ++k) {
-      turn_ = turn_ + 1 < nruns_ ? turn_ + 1 : 0;
-      if (a - run_[turn_].b < kGap) {
-        run_[turn_].b = b;
-        return;
-      }
-    }
-    if (nruns_ < kRuns) {
-      turn_ = nruns_;
-      run_[nruns_++] = Run{a, b};
-    } else {
-      many_ = true;
-    }
-  }
-  bool clash() {
-    if (!many_) {
-      std::sort(run_, run_ + nruns_, [](const Run& x, const Run& y) { return x.a < y.a; });
-      bool apart = true;
-      for (int k = 1; k < nruns_; ++k) apart = apart && run_[k - 1].b <= run_[k].a;
-      if (apart) return false;
-    }
-    std::sort(r_.begin(), r_.end(), [](const R& x, const R& y) { return x.a < y.a; });
-    uintptr_t any = 0, written = 0;
-    for (const R& x : r_) {
-      if (x.a < written || (x.written && x.a < any)) return true;
-      any = std::max(any, x.b);
-      if (x.written) written = std::max(written, x.b);
-    }
-    return false;
-  }
-
- private:
+// Ranges mostly come in a few ascending runs that take turns (tensors cut from
+// flat buffers, or allocated one after another), and then it is enough that no
+// two runs meet. Else they are sorted (1600 ranges: 20 us, more than launching
+// the kernel).
+template <class Each>
+bool ranges_clash(size_t most, Each each) {
   struct R {
     uintptr_t a, b;
     bool written;
   };
-  struct Run {
-    uintptr_t a, b;
-  };
-  static constexpr int kRuns = 16;
-  static constexpr uintptr_t kGap = 1 << 16;
-  std::vector<R> r_;
-  Run run_[kRuns];
-  int nruns_ = 0, turn_ = 0;
-  bool many_ = false;
-};
-
-// Elements a block takes: `least`, or so many that the list makes about
-// `units` blocks; a multiple of 2048.
-int pick_unit(long long total, long long units, long long least) {
-  const long long u = std::max(least, (total + units - 1) / units);
-  return (int)((u + 2047) / 2048 * 2048);
+  constexpr int kRuns = 16;
+  constexpr uintptr_t kGap = 1 << 16;   // between a run's end and its next range
+  const auto before = [](const R& x, const R& y) { return x.a < y.a; };
+  R run[kRuns];
+  int n = 0, turn = 0;
+  bool many = false;
+  each([&](const void* p, size_t bytes, bool) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    for (int k = 0; k < n; ++k) {
+      turn = turn + 1 < n ? turn + 1 : 0;
+      if (a - run[turn].b < kGap) {
+        run[turn].b = a + bytes;
+        return;
+      }
+    }
+    if (n < kRuns) {
+      turn = n;
+      run[n++] = R{a, a + bytes, true};
+    } else {
+      many = true;
+    }
+  });
+  if (!many) {
+    std::sort(run, run + n, before);
+    bool apart = true;
+    for (int k = 1; k < n; ++k) apart = apart && run[k - 1].b <= run[k].a;
+    if (apart) return false;
+  }
+  std::vector<R> r;
+  r.reserve(most);
+  each([&](const void* p, size_t bytes, bool written) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    r.push_back(R{a, a + bytes, written});
+  });
+  std::sort(r.begin(), r.end(), before);
+  uintptr_t any = 0, written = 0;
+  for (const R& x : r) {
+    if (x.a < written || (x.written && x.a < any)) return true;
+    any = std::max(any, x.b);
+    if (x.written) written = std::max(written, x.b);
+  }
+  return false;
 }
 
-long long count_units(const std::vector<GradItem>& it, int unit) {
-  long long u = 0;
-  for (const GradItem& x : it) u += grad_units(x.numel, x.norm_phase, unit);
-  return u;
+// log2 of the elements a block takes: `least`, or so many that the list makes
+// no more than `units` blocks (and one per tensor).
+int pick_unit(long long total, long long units, int least) {
+  int k = least;
+  while ((total >> k) >= units) ++k;
+  return k;
 }
 
 // Whether a list takes the one-kernel form.
@@ -1285,9 +1271,9 @@ bool grad_is_small(const std::vector<GradItem>& it, long long total) {
 }
 
 int enqueue_grad_small(muon_handle* h, const std::vector<GradItem>& it, int kind, bool scale, float max_norm,
-                       float* out, float* per_tensor, double* partials, cudaStream_t st, int* launches) {
+                       float* out, float* per_tensor, cudaStream_t st, int* launches) {
   const int slot = prof_before(h, MUON_KERNEL_GRAD_SMALL, st);
-  MUON_CUDA_TRY(launch_grad_small(it.data(), (int)it.size(), kind, scale, max_norm, out, per_tensor, partials, st));
+  MUON_CUDA_TRY(launch_grad_small(it.data(), (int)it.size(), kind, scale, max_norm, out, per_tensor, st));
   prof_after(h, slot, st);
   ++*launches;
   return MUON_OK;
@@ -1297,43 +1283,37 @@ int enqueue_grad_small(muon_handle* h, const std::vector<GradItem>& it, int kind
 // checked everything.
 int enqueue_grad_norm(muon_handle* h, const std::vector<GradItem>& it, long long total, int kind, float max_norm,
                       float* out, float* per_tensor, double* partials, cudaStream_t st, int* launches) {
-  if (grad_is_small(it, total)) return enqueue_grad_small(h, it, kind, false, max_norm, out, per_tensor, partials, st, launches);
-  // 16 KB for a block: 3.5 GB took 469 us (7.46 TB/s) in units of 16 to 32
+  if (grad_is_small(it, total))
+    return enqueue_grad_small(h, it, kind, false, max_norm, out, per_tensor, st, launches);
+  // 16 KB for a block: 3.5 GB took 469 us (7.46 TB/s) in units of 16 to 64
   // KB, 474 in units of 128 KB; small lists fill the GPU sooner.
   long long bytes = 0;
   for (const GradItem& x : it) bytes += x.numel * (long long)dtype_size(x.stype);
-  const int unit = pick_unit(total, kGradUnits, 2 * bytes > 7 * total ? 4096 : 8192);
-  const long long nunits = count_units(it, unit);
+  const int unit = pick_unit(total, kGradUnits, 2 * bytes > 7 * total ? 12 : 13);
   const int count = (int)it.size();
-  long long base = 0;
-  for (int i0 = 0; i0 < count; i0 += kNormCap) {
+  // Partials, one launch's after another's; then the sums. per_tensor needs
+  // where each launch's partials begin.
+  std::vector<long long> base(1, 0);
+  for (int i0 = 0; i0 < count || i0 == 0; i0 += kNormCap) {
     const int n = std::min(kNormCap, count - i0);
     int units = 0;
-    for (int i = 0; i < n; ++i) units += grad_units(it[i0 + i].numel, it[i0 + i].norm_phase, unit);
-    if (units > 0) {
-      const int slot = prof_before(h, MUON_KERNEL_GRAD_NORM, st);
-      MUON_CUDA_TRY(launch_grad_norm(&it[i0], n, unit, units, kind, partials + base, st));
-      prof_after(h, slot, st);
-      ++*launches;
-    }
-    base += units;
+    const int slot = prof_before(h, MUON_KERNEL_GRAD_NORM, st);
+    MUON_CUDA_TRY(launch_grad_norm(it.data() + i0, n, unit, kind, partials + base.back(), st, &units));
+    prof_after(h, slot, st);
+    if (units > 0) ++*launches;
+    base.push_back(base.back() + units);
   }
-  base = 0;
-  int i0 = 0;
-  do {
-    const int n = std::min(kNormCap, count - i0);
-    const bool last = i0 + n >= count;
-    if (per_tensor || last) {
-      const int slot = prof_before(h, MUON_KERNEL_GRAD_FINISH, st);
-      MUON_CUDA_TRY(launch_grad_finish(it.data() + i0, n, unit, kind, partials, nunits, max_norm,
-                                       last ? out : nullptr, partials + base,
-                                       per_tensor ? per_tensor + i0 : nullptr, st));
-      prof_after(h, slot, st);
-      ++*launches;
-    }
-    for (int i = 0; i < n; ++i) base += grad_units(it[i0 + i].numel, it[i0 + i].norm_phase, unit);
-    i0 += n;
-  } while (i0 < count);
+  for (size_t k = 0; k + 1 < base.size(); ++k) {
+    const int i0 = (int)k * kNormCap, n = std::min(kNormCap, count - i0);
+    const bool last = k + 2 == base.size();
+    if (!per_tensor && !last) continue;
+    const int slot = prof_before(h, MUON_KERNEL_GRAD_FINISH, st);
+    MUON_CUDA_TRY(launch_grad_finish(it.data() + i0, n, unit, kind, partials, base.back(), max_norm,
+                                     last ? out : nullptr, partials + base[k], per_tensor ? per_tensor + i0 : nullptr,
+                                     st));
+    prof_after(h, slot, st);
+    ++*launches;
+  }
   return MUON_OK;
 }
 
@@ -1555,20 +1535,24 @@ int muon_clip_grads(muon_handle* h, const void* const* src, void* const* dst, co
   if (count > 0 && (!src || !dst)) return fail(MUON_ERR_INVALID_ARG, "src and dst are required");
   if ((rc = check_norm_args(norm_kind, max_norm, out, scratch, scratch_bytes, count))) return rc;
   std::vector<GradItem> it((size_t)count);
-  Ranges ranges(2 * (size_t)count);
   for (int i = 0; i < count; ++i) {
     const bool skip = src[i] == nullptr || numels[i] == 0;
     if (!skip) {
-      const size_t ss = dtype_size(src_dtypes[i]), ds = dtype_size(dst_dtypes[i]);
-      if ((rc = check_elem_ptr(src[i], ss, "src", i)) || (rc = check_elem_ptr(dst[i], ds, "dst", i))) return rc;
-      ranges.add(dst[i], (size_t)numels[i] * ds, true);
-      if (src[i] != dst[i]) ranges.add(src[i], (size_t)numels[i] * ss, false);
-      else if (src_dtypes[i] != dst_dtypes[i]) return bad_tensor("dst", i, "is src in another dtype");
+      if ((rc = check_elem_ptr(src[i], dtype_size(src_dtypes[i]), "src", i)) ||
+          (rc = check_elem_ptr(dst[i], dtype_size(dst_dtypes[i]), "dst", i)))
+        return rc;
+      if (src[i] == dst[i] && src_dtypes[i] != dst_dtypes[i]) return bad_tensor("dst", i, "is src in another dtype");
     }
     it[i] = GradItem{src[i], dst[i], skip ? 0 : (long long)numels[i], src_dtypes[i], dst_dtypes[i], 0, 0};
     set_phases(it[i]);
   }
-  if (ranges.clash())
+  if (ranges_clash(2 * it.size(), [&](auto emit) {
+        for (const GradItem& x : it) {
+          if (x.numel == 0) continue;
+          emit(x.dst, (size_t)x.numel * dtype_size(x.dtype), true);
+          if (x.src != x.dst) emit(x.src, (size_t)x.numel * dtype_size(x.stype), false);
+        }
+      }))
     return fail(MUON_ERR_INVALID_ARG, "a written tensor overlaps another tensor of the call (the same one twice?)");
   if (!h) return fail(MUON_ERR_INVALID_ARG, "handle is NULL");
   DeviceGuard g(h->device);
@@ -1578,22 +1562,20 @@ int muon_clip_grads(muon_handle* h, const void* const* src, void* const* dst, co
   int launches = 0;
   double* partials = static_cast<double*>(scratch);
   if (grad_is_small(it, total)) {
-    rc = enqueue_grad_small(h, it, norm_kind, true, max_norm, out, nullptr, partials, st, &launches);
+    rc = enqueue_grad_small(h, it, norm_kind, true, max_norm, out, nullptr, st, &launches);
     h->last_launches = launches;
     return rc;
   }
   if ((rc = enqueue_grad_norm(h, it, total, norm_kind, max_norm, out, nullptr, partials, st, &launches))) return rc;
-  const int unit = pick_unit(total, 1 << 20, 4096);   // 3.5 GB, fp32 / bf16: 1.01 ms; 1.04 / 1.02 in units of 16384
+  const int unit = pick_unit(total, 1 << 20, 12);   // 3.5 GB, fp32 / bf16: 1.01 ms; 1.04 / 1.02 in units of 16384
   // Last tensors first, for what is still in L2 (see g3_scale).
   for (int i1 = count; i1 > 0; i1 -= kScaleCap) {
-    const int i0 = std::max(0, i1 - kScaleCap), n = i1 - i0;
+    const int i0 = std::max(0, i1 - kScaleCap);
     int units = 0;
-    for (int i = i0; i < i1; ++i) units += grad_units(it[i].numel, it[i].scale_phase, unit);
-    if (units == 0) continue;
     const int slot = prof_before(h, MUON_KERNEL_GRAD_SCALE, st);
-    MUON_CUDA_TRY(launch_grad_scale(&it[i0], n, unit, units, out + 1, st));
+    MUON_CUDA_TRY(launch_grad_scale(&it[i0], i1 - i0, unit, out + 1, st, &units));
     prof_after(h, slot, st);
-    ++launches;
+    if (units > 0) ++launches;
   }
   h->last_launches = launches;
   return MUON_OK;
@@ -1618,25 +1600,25 @@ int muon_adamw_step(muon_handle* h, float* const* params, const void* const* gra
   if (reinterpret_cast<uintptr_t>(grad_scale) % 4) return fail(MUON_ERR_INVALID_ARG, "grad_scale is misaligned");
   std::vector<AdamItem> it;
   it.reserve((size_t)count);
-  Ranges ranges(4 * (size_t)count);
   for (int i = 0; i < count; ++i) {
     if (grads[i] == nullptr || numels[i] == 0) continue;
-    const size_t gs = dtype_size(grad_dtypes[i]), n = (size_t)numels[i];
-    if (!(good_elem_ptr(params[i], 4) && good_elem_ptr(grads[i], gs) && good_elem_ptr(exp_avgs[i], 4) &&
-          good_elem_ptr(exp_avg_sqs[i], 4))) {
-      if ((rc = check_elem_ptr(params[i], 4, "params", i)) || (rc = check_elem_ptr(grads[i], gs, "grads", i)) ||
-          (rc = check_elem_ptr(exp_avgs[i], 4, "exp_avgs", i)) ||
-          (rc = check_elem_ptr(exp_avg_sqs[i], 4, "exp_avg_sqs", i)))
-        return rc;
-    }
-    ranges.add(params[i], n * 4, true);
-    ranges.add(exp_avgs[i], n * 4, true);
-    ranges.add(exp_avg_sqs[i], n * 4, true);
-    ranges.add(grads[i], n * gs, false);
-    it.push_back(AdamItem{params[i], grads[i], exp_avgs[i], exp_avg_sqs[i], (long long)n, grad_dtypes[i], 0});
+    const size_t gs = dtype_size(grad_dtypes[i]);
+    if ((rc = check_elem_ptr(params[i], 4, "params", i)) || (rc = check_elem_ptr(grads[i], gs, "grads", i)) ||
+        (rc = check_elem_ptr(exp_avgs[i], 4, "exp_avgs", i)) ||
+        (rc = check_elem_ptr(exp_avg_sqs[i], 4, "exp_avg_sqs", i)))
+      return rc;
+    it.push_back(AdamItem{params[i], grads[i], exp_avgs[i], exp_avg_sqs[i], (long long)numels[i], grad_dtypes[i], 0});
     set_phases(it.back());
   }
-  if (ranges.clash())
+  if (ranges_clash(4 * it.size(), [&](auto emit) {
+        for (const AdamItem& x : it) {
+          const size_t bytes = (size_t)x.numel * 4;
+          emit(x.p, bytes, true);
+          emit(x.m, bytes, true);
+          emit(x.v, bytes, true);
+          emit(x.g, (size_t)x.numel * dtype_size(x.gtype), false);
+        }
+      }))
     return fail(MUON_ERR_INVALID_ARG, "a written tensor overlaps another tensor of the call (the same one twice?)");
   if (!h) return fail(MUON_ERR_INVALID_ARG, "handle is NULL");
   DeviceGuard g(h->device);
@@ -1663,13 +1645,11 @@ int muon_adamw_step(muon_handle* h, float* const* params, const void* const* gra
   int launches = 0;
   // One step of a block's threads: 537 M elements took 2.02 ms, 2.05 in units
   // of 8192; 10 M 43 us, 50.
-  const int unit = pick_unit(total, 1 << 20, 2048);
+  const int unit = pick_unit(total, 1 << 20, 11);
   for (int i1 = (int)it.size(); i1 > 0; i1 -= kAdamCap) {
-    const int i0 = std::max(0, i1 - kAdamCap), n = i1 - i0;
-    int units = 0;
-    for (int i = i0; i < i1; ++i) units += grad_units(it[i].numel, it[i].phase, unit);
+    const int i0 = std::max(0, i1 - kAdamCap);
     const int slot = prof_before(h, MUON_KERNEL_ADAMW, st);
-    MUON_CUDA_TRY(launch_adamw(&it[i0], n, unit, units, a, st));
+    MUON_CUDA_TRY(launch_adamw(&it[i0], i1 - i0, unit, a, st));
     prof_after(h, slot, st);
     ++launches;
   }

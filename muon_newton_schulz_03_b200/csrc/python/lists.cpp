@@ -47,8 +47,7 @@ int type_of(const at::Tensor& t) {
 // Whether a tensor is strided memory on a CUDA device, read as it is. That
 // follows from its set of dispatch keys, so it is asked once per set: nearly
 // all tensors of a program have the same one.
-bool is_plain(const at::Tensor& t) {
-  static thread_local uint64_t known = 0;
+bool is_plain(const at::Tensor& t, uint64_t& known) {
   const uint64_t keys = t.unsafeGetTensorImpl()->key_set().raw_repr();
   if (keys == known) return true;
   if (t.layout() != at::kStrided || !t.is_cuda() || t.is_neg()) return false;
@@ -64,10 +63,11 @@ struct Row {
 
 // A dense strided tensor of an allowed type on the device; `first`: of its
 // row, whose others are laid out like it.
-bool take(PyObject* o, c10::Device device, int allowed, bool first, Row& row, Column& c, size_t i) {
+bool take(PyObject* o, c10::Device device, int allowed, bool first, Row& row, Column& c, size_t i,
+          uint64_t& known) {
   if (!THPVariable_Check(o)) return false;
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (!is_plain(t)) return false;
+  if (!is_plain(t, known)) return false;
   const c10::TensorImpl* impl = t.unsafeGetTensorImpl();
   if (impl->device() != device) return false;
   const int type = type_of(t);
@@ -92,11 +92,15 @@ struct Lists {
   Column col[kMost];
   std::vector<int64_t> numel;
   int n = 0;
+  bool same_ = false;
+  const Column& second() const { return col[same_ ? 0 : 1]; }
   ~Lists() {
     for (PyObject* s : seq) Py_XDECREF(s);
   }
   bool read(PyObject* const* lists, const int* allowed, int count, int64_t device_index) {
     const c10::Device device(at::kCUDA, (c10::DeviceIndex)device_index);
+    same_ = count == 2 && lists[0] == lists[1];   // clipped in place
+    if (same_) count = 1;
     for (int k = 0; k < count; ++k) {
       seq[k] = PySequence_Fast(lists[k], "a list of tensors is needed");
       if (!seq[k]) {
@@ -105,6 +109,7 @@ struct Lists {
       }
       if (PySequence_Fast_GET_SIZE(seq[k]) != PySequence_Fast_GET_SIZE(seq[0])) return false;
     }
+    uint64_t known = 0;
     const Py_ssize_t size = PySequence_Fast_GET_SIZE(seq[0]);
     if (size > INT32_MAX) return false;
     n = (int)size;
@@ -114,10 +119,11 @@ struct Lists {
       PyObject* o = PySequence_Fast_GET_ITEM(seq[0], i);
       if (o == Py_None) continue;
       Row row;
-      if (!take(o, device, allowed[0], true, row, col[0], (size_t)i)) return false;
+      if (!take(o, device, allowed[0], true, row, col[0], (size_t)i, known)) return false;
       numel[i] = THPVariable_Unpack(o).numel();
       for (int k = 1; k < count; ++k)
-        if (!take(PySequence_Fast_GET_ITEM(seq[k], i), device, allowed[k], false, row, col[k], (size_t)i)) return false;
+        if (!take(PySequence_Fast_GET_ITEM(seq[k], i), device, allowed[k], false, row, col[k], (size_t)i, known))
+          return false;
     }
     return true;
   }
@@ -207,27 +213,42 @@ PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const int allowed[2] = {kAny, kAny};
     if (!l.read(&a[2], allowed, 2, device)) Py_RETURN_NONE;
     Buffers b(device, l.n, false);
-    const int rc = c_clip(h, l.col[0].ptr.data(), l.col[1].ptr.data(), l.numel.data(), l.col[0].type.data(),
-                          l.col[1].type.data(), l.n, kind, max_norm, b.out.data_ptr<float>(), b.scratch.data_ptr(),
+    const int rc = c_clip(h, l.col[0].ptr.data(), l.second().ptr.data(), l.numel.data(), l.col[0].type.data(),
+                          l.second().type.data(), l.n, kind, max_norm, b.out.data_ptr<float>(), b.scratch.data_ptr(),
                           b.bytes, c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
     if (rc) return PyLong_FromLong(rc);
     return THPVariable_Wrap(b.out.select(0, 0));
   });
 }
 
-// adamw_step(handle, device, grads, params, exp_avgs, exp_avg_sqs, lr, beta1, beta2, eps, wd, step, step_dev,
-//            grad_scale) -> a status code, or None; step_dev and grad_scale are addresses (0: none)
+// The address of a CUDA tensor of one element of a type; false: it is not that.
+bool one_element(PyObject* o, int64_t device, at::ScalarType type, void** p) {
+  if (!THPVariable_Check(o)) return false;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  uint64_t known = 0;
+  if (!is_plain(t, known) || t.get_device() != device || t.scalar_type() != type || t.numel() != 1) return false;
+  *p = t.data_ptr();
+  return true;
+}
+
+// adamw_step(handle, device, grads, params, exp_avgs, exp_avg_sqs, lr, beta1, beta2, eps, wd, step, grad_scale)
+//   -> a status code, or None; step is an int or a tensor, grad_scale a tensor or None
 PyObject* py_adamw(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  if (!want_args(nargs, 14)) return nullptr;
+  if (!want_args(nargs, 13)) return nullptr;
   return guarded([&]() -> PyObject* {
     muon_handle* h = handle_of(a[0]);
     const int64_t device = PyLong_AsLongLong(a[1]);
     double x[5];
     for (int k = 0; k < 5; ++k) x[k] = PyFloat_AsDouble(a[6 + k]);
-    const int64_t step = PyLong_AsLongLong(a[11]);
-    const void* step_dev = PyLong_AsVoidPtr(a[12]);
-    const void* scale = PyLong_AsVoidPtr(a[13]);
     if (PyErr_Occurred()) return nullptr;
+    int64_t step = 0;
+    void *step_dev = nullptr, *scale = nullptr;
+    if (!one_element(a[11], device, at::kLong, &step_dev)) {
+      if (THPVariable_Check(a[11])) Py_RETURN_NONE;
+      step = PyLong_AsLongLong(a[11]);
+      if (PyErr_Occurred()) return nullptr;
+    }
+    if (a[12] != Py_None && !one_element(a[12], device, at::kFloat, &scale)) Py_RETURN_NONE;
     Lists l;
     const int allowed[4] = {kAny, kF32, kF32, kF32};
     if (!l.read(&a[2], allowed, 4, device)) Py_RETURN_NONE;

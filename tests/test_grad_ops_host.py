@@ -14,7 +14,7 @@ import torch
 import muon_newton_schulz_03_b200 as muon
 from muon_newton_schulz_03_b200 import _bad_lists, _check_scalar, _dense, _grad_dtypes, _norm_kind
 
-GRAD_SCRATCH_DOUBLES = 32768   # MUON_GRAD_SCRATCH_BYTES(count) = 8 * (32768 + count)
+GRAD_SCRATCH_DOUBLES = 65536   # MUON_GRAD_SCRATCH_BYTES(count) = 8 * (65536 + count)
 BASE = 1 << 20      # made-up device addresses: nothing reads them
 SCRATCH = 8 * (GRAD_SCRATCH_DOUBLES + 16)
 
@@ -124,7 +124,7 @@ def _marshal(ts, *more, device=0):
     if not more:
         assert reader.grad_norm(0, device, ts, 0, 1.0, False) is None
     else:
-        assert reader.adamw_step(0, device, ts, *(list(more) * 3)[:3], 1e-3, 0.9, 0.999, 1e-8, 0.0, 1, 0, 0) is None
+        assert reader.adamw_step(0, device, ts, *(list(more) * 3)[:3], 1e-3, 0.9, 0.999, 1e-8, 0.0, 1, None) is None
     _bad_lists(device, [("grads", ts, _grad_dtypes())] + [(f"more{k}", m, (torch.float32,))
                                                           for k, m in enumerate(more)])
 
@@ -188,10 +188,15 @@ def test_dense(t, ok):
 def test_reader_refuses_bad_arguments():
     reader = muon.load_lists()
     for bad in (5, None, [None]):
-        assert reader.adamw_step(0, 0, bad, [], [], [], 1e-3, 0.9, 0.999, 1e-8, 0.0, 1, 0, 0) is None
+        assert reader.adamw_step(0, 0, bad, [], [], [], 1e-3, 0.9, 0.999, 1e-8, 0.0, 1, None) is None
     with pytest.raises(TypeError):
         reader.grad_norm(0, 0)
     with pytest.raises(TypeError):
-        reader.adamw_step(0, 0, [], [], [], [], "x", 0.9, 0.999, 1e-8, 0.0, 1, 0, 0)
+        reader.adamw_step(0, 0, [], [], [], [], "x", 0.9, 0.999, 1e-8, 0.0, 1, None)
+    with pytest.raises(TypeError):
+        reader.adamw_step(0, 0, [], [], [], [], 1e-3, 0.9, 0.999, 1e-8, 0.0, 1.5, None)
+    for scale in (torch.ones(1), 1.0):           # not a CUDA tensor
+        assert reader.adamw_step(0, 0, [], [], [], [], 1e-3, 0.9, 0.999, 1e-8, 0.0, 1, scale) is None
+    assert reader.adamw_step(0, 0, [], [], [], [], 1e-3, 0.9, 0.999, 1e-8, 0.0, torch.ones(1), None) is None
     with pytest.raises(TypeError):
         reader.clip_grads("handle", 0, [], [], 0, 1.0)
