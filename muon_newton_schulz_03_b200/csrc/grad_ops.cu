@@ -52,26 +52,42 @@ template <int kWords>
 struct Words {
   unsigned x[kWords];
 };
-__device__ __forceinline__ Words<8> load_words(const Words<8>* p) {
+// `once`: the lines may leave L2 first, because nothing reads them again soon.
+__device__ __forceinline__ Words<8> load_words(const Words<8>* p, bool once) {
   Words<8> r;
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r.x[0]), "=r"(r.x[1]), "=r"(r.x[2]), "=r"(r.x[3]), "=r"(r.x[4]), "=r"(r.x[5]), "=r"(r.x[6]),
-                 "=r"(r.x[7])
-               : "l"(p)
-               : "memory");
+  if (once)
+    asm volatile("ld.global.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r.x[0]), "=r"(r.x[1]), "=r"(r.x[2]), "=r"(r.x[3]), "=r"(r.x[4]), "=r"(r.x[5]), "=r"(r.x[6]),
+                   "=r"(r.x[7])
+                 : "l"(p)
+                 : "memory");
+  else
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r.x[0]), "=r"(r.x[1]), "=r"(r.x[2]), "=r"(r.x[3]), "=r"(r.x[4]), "=r"(r.x[5]), "=r"(r.x[6]),
+                   "=r"(r.x[7])
+                 : "l"(p)
+                 : "memory");
   return r;
 }
-__device__ __forceinline__ Words<4> load_words(const Words<4>* p) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ Words<4> load_words(const Words<4>* p, bool once) {
+  const uint4* q = reinterpret_cast<const uint4*>(p);
+  const uint4 v = once ? __ldcs(q) : *q;
   return Words<4>{{v.x, v.y, v.z, v.w}};
 }
-__device__ __forceinline__ void store_words(Words<8>* p, const Words<8>& r) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.x[0]), "r"(r.x[1]),
-               "r"(r.x[2]), "r"(r.x[3]), "r"(r.x[4]), "r"(r.x[5]), "r"(r.x[6]), "r"(r.x[7])
-               : "memory");
+__device__ __forceinline__ void store_words(Words<8>* p, const Words<8>& r, bool once) {
+  if (once)
+    asm volatile("st.global.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.x[0]),
+                 "r"(r.x[1]), "r"(r.x[2]), "r"(r.x[3]), "r"(r.x[4]), "r"(r.x[5]), "r"(r.x[6]), "r"(r.x[7])
+                 : "memory");
+  else
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.x[0]), "r"(r.x[1]),
+                 "r"(r.x[2]), "r"(r.x[3]), "r"(r.x[4]), "r"(r.x[5]), "r"(r.x[6]), "r"(r.x[7])
+                 : "memory");
 }
-__device__ __forceinline__ void store_words(Words<4>* p, const Words<4>& r) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(r.x[0], r.x[1], r.x[2], r.x[3]);
+__device__ __forceinline__ void store_words(Words<4>* p, const Words<4>& r, bool once) {
+  uint4* q = reinterpret_cast<uint4*>(p);
+  const uint4 v = make_uint4(r.x[0], r.x[1], r.x[2], r.x[3]);
+  if (once) __stcs(q, v); else *q = v;
 }
 
 // An element type: one element, and the values of a word.
@@ -124,79 +140,120 @@ template <> struct Elem<GRAD_F16> {
 
 // kN consecutive elements at p (on a boundary of their size) as floats, and back.
 template <int kType, int kN>
-__device__ __forceinline__ void load_floats(const void* p, float* v) {
+__device__ __forceinline__ void load_floats(const void* p, float* v, bool once) {
   constexpr int kPer = Elem<kType>::kPerWord;
-  const Words<kN / kPer> r = load_words(static_cast<const Words<kN / kPer>*>(p));
+  const Words<kN / kPer> r = load_words(static_cast<const Words<kN / kPer>*>(p), once);
 #pragma unroll
   for (int k = 0; k < kN / kPer; ++k) Elem<kType>::unpack(r.x[k], v + k * kPer);
 }
 template <int kType, int kN>
-__device__ __forceinline__ void store_floats(void* p, const float* v) {
+__device__ __forceinline__ void store_floats(void* p, const float* v, bool once) {
   constexpr int kPer = Elem<kType>::kPerWord;
   Words<kN / kPer> r;
 #pragma unroll
   for (int k = 0; k < kN / kPer; ++k) r.x[k] = Elem<kType>::pack(v + k * kPer);
-  store_words(static_cast<Words<kN / kPer>*>(p), r);
+  store_words(static_cast<Words<kN / kPer>*>(p), r, once);
 }
 
 // ---------------------------------------------------------------------------
 // Norm
 // ---------------------------------------------------------------------------
 
-// What a block or a thread carries: a sum of squares in fp64, or the largest
-// magnitude as the bits of |g| in fp32 (ordered like the values, NaN above
-// infinity, so that a NaN anywhere is the result).
+// What a block carries: a sum of squares in fp64, or the largest magnitude as
+// the bits of |g| in fp32 (ordered like the values, NaN above infinity, so
+// that a NaN anywhere is the result). Both are 8 bytes: they share the array
+// of partials. Part<kType> is a thread's share of a unit.
 struct SumSq {
   double v;
   static __device__ __forceinline__ SumSq zero() { return SumSq{0.0}; }
-  __device__ __forceinline__ unsigned long long bits() const { return (unsigned long long)__double_as_longlong(v); }
   static __device__ __forceinline__ SumSq load(const SumSq* p) { return SumSq{__ldcg(&p->v)}; }
-  // Eight values.
-  template <int kType> __device__ __forceinline__ void add8(const float* x) {
-    if constexpr (kType != GRAD_F32) {
-      // The products of 16-bit values are exact in fp32; eight of them are
-      // added there (at most 7 roundings of 2^-24), unless the sum is so
-      // large or small that a square may have left fp32's range.
-      float s = 0.0f;
+  __device__ __forceinline__ unsigned long long bits() const { return (unsigned long long)__double_as_longlong(v); }
+  __device__ __forceinline__ void join(const SumSq& o) { v += o.v; }
+  __device__ __forceinline__ SumSq peer(int o) const { return SumSq{__shfl_xor_sync(0xffffffffu, v, o)}; }
+  __device__ __forceinline__ double norm() const { return sqrt(v); }
+
+  template <int kType>
+  struct Part {
+    double v = 0.0;
+    // 32 bytes. 16-bit values: their products are exact in fp32, where two
+    // sums of eight are made, one instruction a value, and joined (at most 8
+    // roundings of 2^-24); unless the sum is so large or small that a square
+    // may have left fp32's range. The pass is bound by HBM, but a long list
+    // of bf16 runs into the board's power limit, so instructions count: 3.5
+    // GB took 557 us when each value was first made an fp32 one, at 1.5 GHz.
+    __device__ __forceinline__ void add(const Words<8>& r) {
+      if constexpr (kType != GRAD_F32) {
+        float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s = fmaf(x[k], x[k], s);
-      if (s > 1e-24f && s < 1e30f) {
-        v += (double)s;
-        return;
+        for (int k = 0; k < 8; k += 2) {
+          s0 = square_add(r.x[k], s0);
+          s1 = square_add(r.x[k + 1], s1);
+        }
+        const float s = s0 + s1;
+        if (s > 1e-24f && s < 1e30f) {
+          v += (double)s;
+          return;
+        }
+        unsigned any = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) any |= r.x[k];
+        if ((any & 0x7fff7fffu) == 0) return;   // all zero
+      }
+      // fp64 per element: an fp32 square can overflow or vanish.
+      constexpr int kPer = Elem<kType>::kPerWord;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float x[kPer];
+        Elem<kType>::unpack(r.x[k], x);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) add1(x[j]);
       }
     }
-    // fp64 per element: an fp32 square can overflow or vanish.
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v += (double)x[k] * (double)x[k];
-  }
-  __device__ __forceinline__ void add1(float x) { v += (double)x * (double)x; }
-  __device__ __forceinline__ void join(const SumSq& o) { v += o.v; }
-  __device__ __forceinline__ SumSq peer(int o) const {
-    SumSq r;
-    r.v = __shfl_xor_sync(0xffffffffu, v, o);
-    return r;
-  }
-  __device__ __forceinline__ double norm() const { return sqrt(v); }
+    static __device__ __forceinline__ float square_add(unsigned w, float s) {
+      const unsigned short lo = (unsigned short)w, hi = (unsigned short)(w >> 16);
+      if constexpr (kType == GRAD_BF16) {
+        asm("fma.rn.f32.bf16 %0, %1, %1, %0;" : "+f"(s) : "h"(lo));
+        asm("fma.rn.f32.bf16 %0, %1, %1, %0;" : "+f"(s) : "h"(hi));
+      } else {
+        asm("fma.rn.f32.f16 %0, %1, %1, %0;" : "+f"(s) : "h"(lo));
+        asm("fma.rn.f32.f16 %0, %1, %1, %0;" : "+f"(s) : "h"(hi));
+      }
+      return s;
+    }
+    __device__ __forceinline__ void add1(float x) { v += (double)x * (double)x; }
+    __device__ __forceinline__ SumSq total() const { return SumSq{v}; }
+  };
 };
 struct MaxAbs {
-  unsigned long long v;   // as wide as SumSq: they share the partials' array
+  unsigned long long v;
   static __device__ __forceinline__ MaxAbs zero() { return MaxAbs{0}; }
-  __device__ __forceinline__ unsigned long long bits() const { return v; }
   static __device__ __forceinline__ MaxAbs load(const MaxAbs* p) { return MaxAbs{__ldcg(&p->v)}; }
-  template <int kType> __device__ __forceinline__ void add8(const float* x) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) add1(x[k]);
-  }
-  __device__ __forceinline__ void add1(float x) {
-    v = max((unsigned)v, __float_as_uint(x) & 0x7fffffffu);
-  }
+  __device__ __forceinline__ unsigned long long bits() const { return v; }
   __device__ __forceinline__ void join(const MaxAbs& o) { v = max((unsigned)v, (unsigned)o.v); }
-  __device__ __forceinline__ MaxAbs peer(int o) const {
-    MaxAbs r;
-    r.v = __shfl_xor_sync(0xffffffffu, (unsigned)v, o);
-    return r;
-  }
+  __device__ __forceinline__ MaxAbs peer(int o) const { return MaxAbs{__shfl_xor_sync(0xffffffffu, (unsigned)v, o)}; }
   __device__ __forceinline__ double norm() const { return (double)__uint_as_float((unsigned)v); }
+
+  template <int kType>
+  struct Part {
+    unsigned wide = 0, pairs = 0;   // bits of |x| in fp32; two 16-bit ones, compared as they are
+    __device__ __forceinline__ void add(const Words<8>& r) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (kType == GRAD_F32) wide = max(wide, r.x[k] & 0x7fffffffu);
+        else pairs = __vmaxu2(pairs, r.x[k] & 0x7fff7fffu);
+      }
+    }
+    __device__ __forceinline__ void add1(float x) { wide = max(wide, __float_as_uint(x) & 0x7fffffffu); }
+    __device__ __forceinline__ MaxAbs total() {
+      if constexpr (kType != GRAD_F32) {
+        float x[2];
+        Elem<kType>::unpack(pairs, x);
+        add1(x[0]);
+        add1(x[1]);
+      }
+      return MaxAbs{wide};
+    }
+  };
 };
 
 // Sum over the block, valid in thread 0.
@@ -222,62 +279,54 @@ __device__ __forceinline__ Acc block_join(Acc a) {
 // (four made blocks wait: 3.5 GB in units of 16 KB took 531 us, two 469), then
 // the rest.
 template <class Acc, int kType, int kStride>
-__device__ __forceinline__ Acc unit_norm(const void* base, long long e0, long long e1, int tid) {
+__device__ __forceinline__ Acc unit_norm(const void* base, long long e0, long long e1, int tid, bool once) {
   typedef Elem<kType> E;
   typedef typename E::T T;
   constexpr int kStep = norm_step(kType);
-  Acc a = Acc::zero();
+  typename Acc::template Part<kType> a;
   const T* p = static_cast<const T*>(base) + e0;
-  const long long n = e1 - e0;
-  const int head = (int)min((long long)((-reinterpret_cast<uintptr_t>(p) & 31) / sizeof(T)), n);
-  const long long nv = (n - head) / kStep;
-  const T* q = p + head;
-  long long i = tid;
+  const int n = (int)(e1 - e0);
+  const int head = min((int)((-reinterpret_cast<uintptr_t>(p) & 31) / sizeof(T)), n);
+  const int nv = (n - head) / kStep;
+  const Words<8>* q = reinterpret_cast<const Words<8>*>(p + head);
+  int i = tid;
   for (; i + kStride < nv; i += 2 * kStride) {
     Words<8> r[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) r[k] = load_words(reinterpret_cast<const Words<8>*>(q) + i + k * kStride);
+    for (int k = 0; k < 2; ++k) r[k] = load_words(q + i + k * kStride, once);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int w = 0; w < 8; w += 8 / E::kPerWord) {
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8 / E::kPerWord; ++j) E::unpack(r[k].x[w + j], x + j * E::kPerWord);
-        a.template add8<kType>(x);
-      }
+    for (int k = 0; k < 2; ++k) a.add(r[k]);
   }
-  if (i < nv) {
-    float x[kStep];
-    load_floats<kType, kStep>(q + i * kStep, x);
-#pragma unroll
-    for (int k = 0; k < kStep; k += 8) a.template add8<kType>(x + k);
-  }
+  if (i < nv) a.add(load_words(q + i, once));
   if (tid < head) a.add1(E::get(p, tid));
-  const long long t = head + nv * kStep + tid;
+  const int t = head + nv * kStep + tid;
   if (t < n) a.add1(E::get(p, t));
-  return a;
+  return a.total();
 }
 
 template <class Acc, int kStride>
-__device__ __forceinline__ Acc unit_norm(int type, const void* base, long long e0, long long e1, int tid) {
+__device__ __forceinline__ Acc unit_norm(int type, const void* base, long long e0, long long e1, int tid,
+                                         bool once) {
   switch (type) {
-    case GRAD_F32: return unit_norm<Acc, GRAD_F32, kStride>(base, e0, e1, tid);
-    case GRAD_BF16: return unit_norm<Acc, GRAD_BF16, kStride>(base, e0, e1, tid);
-    default: return unit_norm<Acc, GRAD_F16, kStride>(base, e0, e1, tid);
+    case GRAD_F32: return unit_norm<Acc, GRAD_F32, kStride>(base, e0, e1, tid, once);
+    case GRAD_BF16: return unit_norm<Acc, GRAD_BF16, kStride>(base, e0, e1, tid, once);
+    default: return unit_norm<Acc, GRAD_F16, kStride>(base, e0, e1, tid, once);
   }
 }
 
+// Eight blocks an SM: 3.5 GB of bf16 took 480 us with 30 registers a thread,
+// 495 with the 38 that the compiler would take.
 template <class Acc, int kCap>
-__global__ void __launch_bounds__(kThreads) g1_norm(const __grid_constant__ GradTable<kCap> t, int unit,
-                                                    Acc* __restrict__ partials) {
+__global__ void __launch_bounds__(kThreads, 8) g1_norm(const __grid_constant__ GradTable<kCap> t, int unit,
+                                                       int keep_from, Acc* __restrict__ partials) {
   const int blk = blockIdx.x;
   const int i = find_tensor(t.units, blk);
   const unsigned long long meta = t.meta[i];
   const UnitRange r = unit_range(meta, blk - t.units.unit0[i], unit);
   dep_wait();
   dep_release();
-  const Acc a = block_join<Acc, kThreads>(unit_norm<Acc, kThreads>(grad_src(meta), t.src[i], r.e0, r.e1, threadIdx.x));
+  const Acc a = block_join<Acc, kThreads>(
+      unit_norm<Acc, kThreads>(grad_src(meta), t.src[i], r.e0, r.e1, threadIdx.x, blk < keep_from));
   if (threadIdx.x == 0) partials[blk] = a;
 }
 
@@ -362,7 +411,8 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kFinish
 
 // dst = s * src over a unit, each element rounded once to dst's type.
 template <int kSrc, int kDst, int kStride>
-__device__ __forceinline__ void unit_scale(const void* src, void* dst, const UnitRange& u, float s, int tid) {
+__device__ __forceinline__ void unit_scale(const void* src, void* dst, const UnitRange& u, float s, int tid,
+                                           bool once) {
   typedef Elem<kSrc> S;
   typedef Elem<kDst> D;
   constexpr int kStep = scale_step(kSrc, kDst);
@@ -371,10 +421,10 @@ __device__ __forceinline__ void unit_scale(const void* src, void* dst, const Uni
   typename D::T* out = static_cast<typename D::T*>(dst) + b;
   for (long long i = tid; i < nv; i += kStride) {
     float x[kStep];
-    load_floats<kSrc, kStep>(in + i * kStep, x);
+    load_floats<kSrc, kStep>(in + i * kStep, x, once);
 #pragma unroll
     for (int k = 0; k < kStep; ++k) x[k] *= s;
-    store_floats<kDst, kStep>(out + i * kStep, x);
+    store_floats<kDst, kStep>(out + i * kStep, x, once);
   }
   const long long e = b + nv * kStep + tid;
   if (e < u.e1) D::put(dst, e, S::get(src, e) * s);
@@ -384,27 +434,27 @@ __device__ __forceinline__ void unit_scale(const void* src, void* dst, const Uni
 
 template <int kSrc, int kStride>
 __device__ __forceinline__ void unit_scale_to(int dst_type, const void* src, void* dst, const UnitRange& u, float s,
-                                              int tid) {
+                                              int tid, bool once) {
   switch (dst_type) {
-    case GRAD_F32: unit_scale<kSrc, GRAD_F32, kStride>(src, dst, u, s, tid); break;
-    case GRAD_BF16: unit_scale<kSrc, GRAD_BF16, kStride>(src, dst, u, s, tid); break;
-    default: unit_scale<kSrc, GRAD_F16, kStride>(src, dst, u, s, tid); break;
+    case GRAD_F32: unit_scale<kSrc, GRAD_F32, kStride>(src, dst, u, s, tid, once); break;
+    case GRAD_BF16: unit_scale<kSrc, GRAD_BF16, kStride>(src, dst, u, s, tid, once); break;
+    default: unit_scale<kSrc, GRAD_F16, kStride>(src, dst, u, s, tid, once); break;
   }
 }
 
 template <int kStride>
 __device__ __forceinline__ void unit_scale(unsigned long long meta, const void* src, void* dst, const UnitRange& u,
-                                           float s, int tid) {
+                                           float s, int tid, bool once) {
   if (s == 1.0f && src == dst) return;   // in place and inside the bound: nothing changes
   switch (grad_src(meta)) {
-    case GRAD_F32: unit_scale_to<GRAD_F32, kStride>(grad_dst(meta), src, dst, u, s, tid); break;
-    case GRAD_BF16: unit_scale_to<GRAD_BF16, kStride>(grad_dst(meta), src, dst, u, s, tid); break;
-    default: unit_scale_to<GRAD_F16, kStride>(grad_dst(meta), src, dst, u, s, tid); break;
+    case GRAD_F32: unit_scale_to<GRAD_F32, kStride>(grad_dst(meta), src, dst, u, s, tid, once); break;
+    case GRAD_BF16: unit_scale_to<GRAD_BF16, kStride>(grad_dst(meta), src, dst, u, s, tid, once); break;
+    default: unit_scale_to<GRAD_F16, kStride>(grad_dst(meta), src, dst, u, s, tid, once); break;
   }
 }
 
 template <int kCap>
-__global__ void __launch_bounds__(kThreads) g3_scale(const __grid_constant__ ScaleTable<kCap> t, int unit,
+__global__ void __launch_bounds__(kThreads) g3_scale(const __grid_constant__ ScaleTable<kCap> t, int unit, int once,
                                                      const float* __restrict__ scale) {
   // Last unit first: what the norm's pass read last is still in L2.
   const int blk = (int)(gridDim.x - 1 - blockIdx.x);
@@ -413,7 +463,7 @@ __global__ void __launch_bounds__(kThreads) g3_scale(const __grid_constant__ Sca
   const UnitRange r = unit_range(meta, blk - t.units.unit0[i], unit);
   dep_wait();
   dep_release();
-  unit_scale<kThreads>(meta, t.src[i], t.dst[i], r, __ldcg(scale), threadIdx.x);
+  unit_scale<kThreads>(meta, t.src[i], t.dst[i], r, __ldcg(scale), threadIdx.x, once != 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -449,7 +499,7 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kSmallT
     const int i = find_tensor(t.units, u);
     const unsigned long long meta = t.meta[i];
     const UnitRange r = unit_range(meta, u - t.units.unit0[i], kGradSmallUnit);
-    Acc a = unit_norm<Acc, 32>(grad_src(meta), t.src[i], r.e0, r.e1, lane);
+    Acc a = unit_norm<Acc, 32>(grad_src(meta), t.src[i], r.e0, r.e1, lane, false);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a.join(a.peer(o));
     __syncwarp();
@@ -481,7 +531,7 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kSmallT
       const int i = find_tensor(t.units, u);
       const unsigned long long meta = t.meta[i];
       const UnitRange r = unit_range(meta, u - t.units.unit0[i], kGradSmallUnit);
-      unit_scale<32>(meta, t.src[i], t.dst[i], r, s, lane);
+      unit_scale<32>(meta, t.src[i], t.dst[i], r, s, lane, false);
     }
   } else if (per_tensor != nullptr) {
     for (int i = warp; i < t.units.count; i += kWarps) {
@@ -512,22 +562,22 @@ struct AdamW {
 // A unit: 8 elements at a time, 32 bytes of each fp32 tensor.
 template <int kType>
 __device__ __forceinline__ void unit_adamw(float* p, const void* g, float* m, float* v, const UnitRange& u,
-                                           const AdamW& f) {
+                                           const AdamW& f, bool once) {
   typedef Elem<kType> E;
   constexpr int kStep = kAdamStep;
   const long long b = u.e0 + u.head, nv = (u.e1 - b) / kStep;
   for (long long i = threadIdx.x; i < nv; i += kThreads) {
     const long long e = b + i * kStep;
     float gx[kStep], px[kStep], mx[kStep], vx[kStep];
-    load_floats<kType, kStep>(static_cast<const typename E::T*>(g) + e, gx);
-    load_floats<GRAD_F32, kStep>(p + e, px);
-    load_floats<GRAD_F32, kStep>(m + e, mx);
-    load_floats<GRAD_F32, kStep>(v + e, vx);
+    load_floats<kType, kStep>(static_cast<const typename E::T*>(g) + e, gx, once);
+    load_floats<GRAD_F32, kStep>(p + e, px, once);
+    load_floats<GRAD_F32, kStep>(m + e, mx, once);
+    load_floats<GRAD_F32, kStep>(v + e, vx, once);
 #pragma unroll
     for (int k = 0; k < kStep; ++k) f(px[k], mx[k], vx[k], gx[k]);
-    store_floats<GRAD_F32, kStep>(p + e, px);
-    store_floats<GRAD_F32, kStep>(m + e, mx);
-    store_floats<GRAD_F32, kStep>(v + e, vx);
+    store_floats<GRAD_F32, kStep>(p + e, px, once);
+    store_floats<GRAD_F32, kStep>(m + e, mx, once);
+    store_floats<GRAD_F32, kStep>(v + e, vx, once);
   }
   const long long e = b + nv * kStep + threadIdx.x;
   if (e < u.e1) f(p[e], m[e], v[e], E::get(g, e));
@@ -558,9 +608,9 @@ __global__ void __launch_bounds__(kThreads) g4_adamw(const __grid_constant__ Ada
     f.rsqrt_bc2 = corr[1];
   }
   switch (grad_src(meta)) {
-    case GRAD_F32: unit_adamw<GRAD_F32>(t.p[i], t.g[i], t.m[i], t.v[i], r, f); break;
-    case GRAD_BF16: unit_adamw<GRAD_BF16>(t.p[i], t.g[i], t.m[i], t.v[i], r, f); break;
-    default: unit_adamw<GRAD_F16>(t.p[i], t.g[i], t.m[i], t.v[i], r, f); break;
+    case GRAD_F32: unit_adamw<GRAD_F32>(t.p[i], t.g[i], t.m[i], t.v[i], r, f, a.once != 0); break;
+    case GRAD_BF16: unit_adamw<GRAD_BF16>(t.p[i], t.g[i], t.m[i], t.v[i], r, f, a.once != 0); break;
+    default: unit_adamw<GRAD_F16>(t.p[i], t.g[i], t.m[i], t.v[i], r, f, a.once != 0); break;
   }
 }
 
@@ -614,7 +664,7 @@ void fill(ScaleTable<kCap>& t, const GradItem* it, int n, int unit) {
 }
 
 template <class Acc, int kCap>
-cudaError_t norm_launch(const GradItem* it, int n, int unit, double* partials, cudaStream_t st, int* units) {
+cudaError_t norm_launch(const GradItem* it, int n, int unit, int keep, double* partials, cudaStream_t st, int* units) {
   GradTable<kCap> t;
   for (int i = 0; i < n; ++i) {
     t.src[i] = it[i].src;
@@ -623,7 +673,8 @@ cudaError_t norm_launch(const GradItem* it, int n, int unit, double* partials, c
   fill_index(t.units, n, [&](int i) { return grad_units(it[i].numel, it[i].norm_phase, unit); });
   *units = t.units.unit0[n];
   if (*units == 0) return cudaSuccess;
-  return launch_dep(g1_norm<Acc, kCap>, (unsigned)*units, kThreads, st, t, unit, reinterpret_cast<Acc*>(partials));
+  return launch_dep(g1_norm<Acc, kCap>, (unsigned)*units, kThreads, st, t, unit, *units - keep,
+                    reinterpret_cast<Acc*>(partials));
 }
 
 template <class Acc, int kCap>
@@ -640,12 +691,13 @@ cudaError_t finish_launch(const GradItem* it, int n, int unit, const double* all
 }
 
 template <int kCap>
-cudaError_t scale_launch(const GradItem* it, int n, int unit, const float* scale, cudaStream_t st, int* units) {
+cudaError_t scale_launch(const GradItem* it, int n, int unit, int once, const float* scale, cudaStream_t st,
+                         int* units) {
   ScaleTable<kCap> t;
   fill(t, it, n, unit);
   *units = t.units.unit0[n];
   if (*units == 0) return cudaSuccess;
-  return launch_dep(g3_scale<kCap>, (unsigned)*units, kThreads, st, t, unit, scale);
+  return launch_dep(g3_scale<kCap>, (unsigned)*units, kThreads, st, t, unit, once, scale);
 }
 
 template <class Acc, int kCap>
@@ -672,10 +724,10 @@ cudaError_t adamw_launch(const AdamItem* it, int n, int unit, const AdamArgs& a,
 }
 
 template <class Acc>
-cudaError_t norm_for(const GradItem* it, int n, int unit, double* partials, cudaStream_t st, int* units) {
-  if (n <= kGradCapSmall) return norm_launch<Acc, kGradCapSmall>(it, n, unit, partials, st, units);
-  if (n <= kGradCapMid) return norm_launch<Acc, kGradCapMid>(it, n, unit, partials, st, units);
-  return norm_launch<Acc, kNormCap>(it, n, unit, partials, st, units);
+cudaError_t norm_for(const GradItem* it, int n, int unit, int keep, double* partials, cudaStream_t st, int* units) {
+  if (n <= kGradCapSmall) return norm_launch<Acc, kGradCapSmall>(it, n, unit, keep, partials, st, units);
+  if (n <= kGradCapMid) return norm_launch<Acc, kGradCapMid>(it, n, unit, keep, partials, st, units);
+  return norm_launch<Acc, kNormCap>(it, n, unit, keep, partials, st, units);
 }
 
 template <class Acc>
@@ -696,10 +748,10 @@ cudaError_t small_for(const GradItem* it, int n, bool scale, float max_norm, flo
 
 }  // namespace
 
-cudaError_t launch_grad_norm(const GradItem* it, int n, int unit, int kind, double* partials, cudaStream_t st,
-                             int* units) {
-  return kind == GRAD_NORM_INF ? norm_for<MaxAbs>(it, n, unit, partials, st, units)
-                               : norm_for<SumSq>(it, n, unit, partials, st, units);
+cudaError_t launch_grad_norm(const GradItem* it, int n, int unit, int keep, int kind, double* partials,
+                             cudaStream_t st, int* units) {
+  return kind == GRAD_NORM_INF ? norm_for<MaxAbs>(it, n, unit, keep, partials, st, units)
+                               : norm_for<SumSq>(it, n, unit, keep, partials, st, units);
 }
 
 cudaError_t launch_grad_finish(const GradItem* it, int n, int unit, int kind, const double* all, long long nunits,
@@ -716,10 +768,11 @@ cudaError_t launch_grad_small(const GradItem* it, int n, int kind, bool scale, f
                                : small_for<SumSq>(it, n, scale, max_norm, out, per_tensor, st);
 }
 
-cudaError_t launch_grad_scale(const GradItem* it, int n, int unit, const float* scale, cudaStream_t st, int* units) {
-  if (n <= kGradCapSmall) return scale_launch<kGradCapSmall>(it, n, unit, scale, st, units);
-  if (n <= kGradCapMid) return scale_launch<kGradCapMid>(it, n, unit, scale, st, units);
-  return scale_launch<kScaleCap>(it, n, unit, scale, st, units);
+cudaError_t launch_grad_scale(const GradItem* it, int n, int unit, int once, const float* scale, cudaStream_t st,
+                              int* units) {
+  if (n <= kGradCapSmall) return scale_launch<kGradCapSmall>(it, n, unit, once, scale, st, units);
+  if (n <= kGradCapMid) return scale_launch<kGradCapMid>(it, n, unit, once, scale, st, units);
+  return scale_launch<kScaleCap>(it, n, unit, once, scale, st, units);
 }
 
 cudaError_t launch_adamw(const AdamItem* it, int n, int unit, const AdamArgs& a, cudaStream_t st) {

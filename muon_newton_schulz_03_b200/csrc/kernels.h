@@ -296,13 +296,15 @@ struct AdamArgs {
   float step_size, rsqrt_bc2;       // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t); unused with `step`
   const long long* step;            // device step number, or NULL
   const float* grad_scale;          // device multiplier of the gradients, or NULL
+  int once;                         // nothing of the lists is read again soon
 };
 
 // Each launches one kernel over up to the table's capacity of tensors, in
 // units of 2^unit elements; *units receives their number (0: no launch).
 // Partial k of the launch is the norm of its unit k.
-cudaError_t launch_grad_norm(const GradItem* it, int n, int unit, int kind, double* partials, cudaStream_t st,
-                             int* units);
+// The last `keep` units stay in L2 where they can, for the pass that follows.
+cudaError_t launch_grad_norm(const GradItem* it, int n, int unit, int keep, int kind, double* partials,
+                             cudaStream_t st, int* units);
 // out (or NULL): norm and clip multiplier over all `nunits` partials at `all`.
 // per_tensor (or NULL): norms of these n tensors, whose partials start at `partials`.
 cudaError_t launch_grad_finish(const GradItem* it, int n, int unit, int kind, const double* all, long long nunits,
@@ -312,7 +314,9 @@ cudaError_t launch_grad_finish(const GradItem* it, int n, int unit, int kind, co
 // lists of up to kGradCapMid tensors and kGradSmallNumel elements.
 cudaError_t launch_grad_small(const GradItem* it, int n, int kind, bool scale, float max_norm, float* out,
                               float* per_tensor, cudaStream_t st);
-cudaError_t launch_grad_scale(const GradItem* it, int n, int unit, const float* scale, cudaStream_t st, int* units);
+// once: nothing of the list is read again soon.
+cudaError_t launch_grad_scale(const GradItem* it, int n, int unit, int once, const float* scale, cudaStream_t st,
+                              int* units);
 cudaError_t launch_adamw(const AdamItem* it, int n, int unit, const AdamArgs& a, cudaStream_t st);
 
 // Sets the calling thread's muon_last_error text.

@@ -1175,6 +1175,12 @@ int step_impl(muon_handle* h, float* const* params, const void* const* grads, fl
 // ---- Operators on lists of gradients ----
 
 constexpr long long kGradMaxNumel = 1ll << 40;   // of one list
+// Half of L2. The norm's pass leaves so many bytes of its gradients there
+// (earlier ones leave first), and a longer pass after it marks what it moves
+// to leave first: clipping 30 M fp16 elements into fp32 took 43.3 us, 49.2
+// without either, the clipped AdamW of a 50001 x 768 table 180 us, 185; lists
+// of gigabytes are level.
+constexpr double kGradL2 = 64.0 * (1 << 20);
 
 int bad_tensor(const char* what, int i, const char* why) {
   return fail(MUON_ERR_INVALID_ARG, std::string(what) + "[" + std::to_string(i) + "] " + why);
@@ -1290,6 +1296,8 @@ int enqueue_grad_norm(muon_handle* h, const std::vector<GradItem>& it, long long
   long long bytes = 0;
   for (const GradItem& x : it) bytes += x.numel * (long long)dtype_size(x.stype);
   const int unit = pick_unit(total, kGradUnits, 2 * bytes > 7 * total ? 12 : 13);
+  // What the pass over the same gradients that follows finds in L2.
+  const int keep = (int)(total > 0 ? std::min(1.0 * (1 << 30), kGradL2 / ((double)bytes / (double)total) / (1 << unit)) : 0);
   const int count = (int)it.size();
   // Partials, one launch's after another's; then the sums. per_tensor needs
   // where each launch's partials begin.
@@ -1298,7 +1306,7 @@ int enqueue_grad_norm(muon_handle* h, const std::vector<GradItem>& it, long long
     const int n = std::min(kNormCap, count - i0);
     int units = 0;
     const int slot = prof_before(h, MUON_KERNEL_GRAD_NORM, st);
-    MUON_CUDA_TRY(launch_grad_norm(it.data() + i0, n, unit, kind, partials + base.back(), st, &units));
+    MUON_CUDA_TRY(launch_grad_norm(it.data() + i0, n, unit, keep, kind, partials + base.back(), st, &units));
     prof_after(h, slot, st);
     if (units > 0) ++*launches;
     base.push_back(base.back() + units);
@@ -1567,13 +1575,18 @@ int muon_clip_grads(muon_handle* h, const void* const* src, void* const* dst, co
     return rc;
   }
   if ((rc = enqueue_grad_norm(h, it, total, norm_kind, max_norm, out, nullptr, partials, st, &launches))) return rc;
-  const int unit = pick_unit(total, 1 << 20, 12);   // 3.5 GB, fp32 / bf16: 1.01 ms; 1.04 / 1.02 in units of 16384
+  // 16 or 32 KB of a list for a block, whose threads first wait for the
+  // multiplier: 872 M bf16 elements took 506 us, 600 in units of 8 KB.
+  const int unit = pick_unit(total, 1 << 20, 13);
+  double bytes = 0.0;
+  for (const GradItem& x : it) bytes += (double)x.numel * (double)(dtype_size(x.stype) + dtype_size(x.dtype));
+  const int once = bytes > kGradL2;
   // Last tensors first, for what is still in L2 (see g3_scale).
   for (int i1 = count; i1 > 0; i1 -= kScaleCap) {
     const int i0 = std::max(0, i1 - kScaleCap);
     int units = 0;
     const int slot = prof_before(h, MUON_KERNEL_GRAD_SCALE, st);
-    MUON_CUDA_TRY(launch_grad_scale(&it[i0], i1 - i0, unit, out + 1, st, &units));
+    MUON_CUDA_TRY(launch_grad_scale(&it[i0], i1 - i0, unit, once, out + 1, st, &units));
     prof_after(h, slot, st);
     if (units > 0) ++launches;
   }
@@ -1640,6 +1653,7 @@ int muon_adamw_step(muon_handle* h, float* const* params, const void* const* gra
     a.rsqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
   }
   a.grad_scale = grad_scale;
+  a.once = (double)total * 28.0 > kGradL2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   prof_call_begin(h);
   int launches = 0;

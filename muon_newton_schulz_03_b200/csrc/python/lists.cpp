@@ -80,9 +80,14 @@ bool take(PyObject* o, c10::Device device, int allowed, bool first, Row& row, Co
     if (impl->sizes() != row.sizes) return false;
     if (!(contiguous && row.contiguous) && impl->strides() != row.strides) return false;
   }
-  c.ptr[i] = t.data_ptr();
+  // data_ptr(), without looking the element size up
+  const c10::Storage& storage = impl->unsafe_storage();
+  char* base = storage ? static_cast<char*>(storage.unsafeGetStorageImpl()->mutable_data()) : nullptr;
   c.type[i] = type;
-  return c.ptr[i] != nullptr || impl->numel() == 0;
+  if (impl->numel() == 0) return true;
+  if (base == nullptr) return false;
+  c.ptr[i] = base + impl->storage_offset() * (type == MUON_DTYPE_F32 ? 4 : 2);
+  return true;
 }
 
 // Paired lists; where the first holds None, the entry is skipped.

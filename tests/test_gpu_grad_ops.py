@@ -3,8 +3,9 @@
 Tolerances count roundings (u = 2^-24, half an fp32 step; half a step of the
 written type for its last rounding):
 * norm: fp32 gradients are summed in fp64, so the result is one rounding off;
-  16-bit ones are added in eights in fp32, at most 7 u on the sum and 3.5 u on
-  its root, and one rounding more. Magnitudes are exact.
+  16-bit ones are added in sixteens in fp32 (two sums of eight, joined: their
+  products are exact, so at most 8 roundings), 8 u on the sum and 4 u on its
+  root, and one rounding more. Magnitudes are exact.
 * multiplier: the norm's error and one rounding; clipped values: that, one
   fp32 product, one rounding to the written type (an absolute half step below
   its smallest normal number).
@@ -54,7 +55,7 @@ def exact_norm(ts, kind=2.0):
 def norm_tol(ts, kind):
     if kind == math.inf:
         return 0.0
-    return (4.5 if any(t.dtype != F32 for t in ts) else 1.0) * U * 1.001
+    return (5.0 if any(t.dtype != F32 for t in ts) else 1.0) * U * 1.001
 
 
 def clip_of(norm, max_norm):
@@ -97,7 +98,7 @@ def test_norm_beyond_the_range_of_fp32_squares(opt, dtype, mag):
     ts = tensors([5, 4097], (dtype,), seed=4, scale=mag)
     norm, _ = opt.grad_norm(ts)
     want, _ = exact_norm(ts)
-    assert abs(norm.item() - want) <= 4.5 * U * 1.001 * want
+    assert abs(norm.item() - want) <= 5.0 * U * 1.001 * want
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
@@ -397,7 +398,7 @@ def test_captured_training_tail(opt):
         torch.cuda.synchronize()
         assert step.item() == t
         norm = exact_norm(g)[0]
-        assert abs(scale.item() - clip_of(norm, bound)) <= 6.5 * U * 1.001
+        assert abs(scale.item() - clip_of(norm, bound)) <= 7.0 * U * 1.001
         for i in range(len(p)):
             want, tol = adamw64(old[0][i], g[i], old[1][i], old[2][i], step=t, s=scale.item(), **hyper)
             check_adamw((p[i], m[i], v[i]), want, tol)
@@ -450,7 +451,7 @@ def test_more_than_2_to_31_elements(opt, dtype):
     g[(1 << 31) + 1] = -32.0
     want = math.sqrt(0.25 * (n - 2) + 64.0 ** 2 + 32.0 ** 2)
     norm, _ = opt.grad_norm([g])
-    assert abs(norm.item() - want) <= 4.5 * U * 1.001 * want
+    assert abs(norm.item() - want) <= 5.0 * U * 1.001 * want
     assert opt.grad_norm([g], norm_type=math.inf)[0].item() == 64.0
     p = torch.full((n,), 1.0, device=DEV)
     m, v = torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
