@@ -250,9 +250,8 @@ int muon_step_scaled(muon_handle* h, float* const* params,
 /* ---- Gradients of the whole model, and the tensors Muon does not take ----
  *
  * Muon updates the 2D hidden matrices; embeddings, heads, norms and biases
- * go to AdamW ("Why Muon Works", "2D hidden -> Muon, the rest -> AdamW"),
- * and clipping looks at all of them together ("Por que AdamW ...", gradient
- * clipping). The calls below take lists of tensors of any shape: tensor i is
+ * go to AdamW ("Why Muon Works": hybrid routing), and clipping looks at all
+ * of them together. The calls below take lists of tensors of any shape: tensor i is
  * numels[i] (>= 0) consecutive elements of type dtypes[i], aligned to its
  * element size; 2^40 elements at most in all. count may be 0. The arrays are
  * host arrays, read during the call only. Nothing is allocated, uploaded or
@@ -270,8 +269,12 @@ enum muon_norm_kind {
   MUON_NORM_INF = 1 /* largest magnitude                                    */
 };
 
-/* Bytes of device scratch for a list of `count` tensors. */
+/* Bytes of device scratch for a list of `count` tensors. A list of at most
+ * MUON_GRAD_SMALL_COUNT tensors and MUON_GRAD_SMALL_NUMEL elements (NULL ones
+ * count too) takes one kernel and needs none. */
 #define MUON_GRAD_SCRATCH_BYTES(count) ((size_t)8 * ((size_t)65536 + (size_t)(count)))
+#define MUON_GRAD_SMALL_COUNT 256
+#define MUON_GRAD_SMALL_NUMEL 131072
 
 /* Norm of all tensors together and its clip multiplier.
  *   tensors    : device pointers; NULL skips tensor i (it adds nothing).
@@ -283,8 +286,8 @@ enum muon_norm_kind {
  *   per_tensor : device float[count] or NULL: every tensor's norm (0 for a
  *                skipped one).
  *   scratch    : device memory, 8-byte aligned, scratch_bytes >=
- *                MUON_GRAD_SCRATCH_BYTES(count); free for other use once the
- *                stream has passed the call. */
+ *                MUON_GRAD_SCRATCH_BYTES(count) (NULL and 0 for a small list);
+ *                free for other use once the stream has passed the call. */
 int muon_grad_norm(muon_handle* h, const void* const* tensors,
                    const int64_t* numels, const int32_t* dtypes, int count,
                    int norm_kind, float max_norm, float* out,

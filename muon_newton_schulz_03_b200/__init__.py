@@ -26,6 +26,7 @@ lines").
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 from ._lib import EXPORTED, MuonConfig, MuonError, check, lib_path, load, load_lists
@@ -153,7 +154,12 @@ def _grad_dtypes():
 
 
 def _sequence(ts):
-    return ts if isinstance(ts, (list, tuple)) else list(ts)
+    if isinstance(ts, (list, tuple)):
+        return ts
+    import torch
+    if isinstance(ts, torch.Tensor):
+        raise TypeError("a list of tensors is needed, got a tensor")
+    return list(ts)
 
 
 def _dense(t):
@@ -342,7 +348,6 @@ class Muon:
         check(self._lib.muon_init(int(device), ctypes.byref(cfg), ctypes.byref(h)))
         self._h = h
         self._hv = h.value
-        self._lists = load_lists()
         self.device = device
         self.ns_precision = ns_precision
         self.small_path = bool(small_path)
@@ -418,6 +423,10 @@ class Muon:
                                          _stream_handle(stream)))
 
     # -- gradients of the whole model, and the tensors Muon does not take ----
+    @functools.cached_property
+    def _lists(self):
+        return load_lists()
+
     def _on(self, stream):
         """Context in which the given stream is the current one."""
         import torch
@@ -434,7 +443,9 @@ class Muon:
         (1 without a ``max_norm``), and with ``per_tensor`` a third, the
         norm of each tensor (0 for a ``None``). Nothing waits for the GPU;
         pass ``scale`` on as ``grad_scale``. A NaN or infinity among the
-        entries makes the norm NaN or infinite, the multiplier NaN or 0.
+        entries makes the norm NaN or infinite, the multiplier NaN or 0. The
+        call runs on ``stream`` (default: the handle's device's current one);
+        its results belong to that stream.
         """
         if stream is not None:
             with self._on(stream):

@@ -121,7 +121,7 @@ def build_lists(force: bool = False, verbose: bool = False) -> str:
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     os.makedirs(BUILD_DIR, exist_ok=True)
     lib = os.path.join(home, "lib")
-    tmp = LISTS_PATH + ".tmp"
+    tmp = f"{LISTS_PATH}.{os.getpid()}.tmp"
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
            "-isystem", os.path.join(home, "include"),

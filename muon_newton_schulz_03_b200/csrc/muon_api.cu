@@ -1272,8 +1272,9 @@ int pick_unit(long long total, long long units, int least) {
 }
 
 // Whether a list takes the one-kernel form.
-bool grad_is_small(const std::vector<GradItem>& it, long long total) {
-  return (int)it.size() <= kGradCapMid && total <= kGradSmallNumel;
+bool grad_is_small(int count, long long total) {
+  static_assert(MUON_GRAD_SMALL_COUNT == kGradCapMid && MUON_GRAD_SMALL_NUMEL == kGradSmallNumel, "small lists");
+  return count <= kGradCapMid && total <= kGradSmallNumel;
 }
 
 int enqueue_grad_small(muon_handle* h, const std::vector<GradItem>& it, int kind, bool scale, float max_norm,
@@ -1289,7 +1290,7 @@ int enqueue_grad_small(muon_handle* h, const std::vector<GradItem>& it, int kind
 // checked everything.
 int enqueue_grad_norm(muon_handle* h, const std::vector<GradItem>& it, long long total, int kind, float max_norm,
                       float* out, float* per_tensor, double* partials, cudaStream_t st, int* launches) {
-  if (grad_is_small(it, total))
+  if (grad_is_small((int)it.size(), total))
     return enqueue_grad_small(h, it, kind, false, max_norm, out, per_tensor, st, launches);
   // 16 KB for a block: 3.5 GB took 469 us (7.46 TB/s) in units of 16 to 64
   // KB, 474 in units of 128 KB; small lists fill the GPU sooner.
@@ -1326,10 +1327,11 @@ int enqueue_grad_norm(muon_handle* h, const std::vector<GradItem>& it, long long
 }
 
 int check_norm_args(int norm_kind, float max_norm, const float* out, const void* scratch, size_t scratch_bytes,
-                    int count) {
+                    int count, long long total) {
   if (norm_kind != MUON_NORM_L2 && norm_kind != MUON_NORM_INF) return fail(MUON_ERR_INVALID_ARG, "unknown norm_kind");
   if (!(max_norm >= 0.0f)) return fail(MUON_ERR_INVALID_ARG, "max_norm must be >= 0 (infinity: no bound)");
   if (!out || reinterpret_cast<uintptr_t>(out) % 4) return fail(MUON_ERR_INVALID_ARG, "out is NULL or misaligned");
+  if (grad_is_small(count, total)) return MUON_OK;
   if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 8)
     return fail(MUON_ERR_INVALID_ARG, "scratch is NULL or not 8-byte aligned");
   const size_t need = MUON_GRAD_SCRATCH_BYTES(count);
@@ -1510,7 +1512,7 @@ int muon_grad_norm(muon_handle* h, const void* const* tensors, const int64_t* nu
   long long total = 0;
   if ((rc = check_list(numels, dtypes, count, "tensors", &total))) return rc;
   if (count > 0 && !tensors) return fail(MUON_ERR_INVALID_ARG, "tensors is NULL");
-  if ((rc = check_norm_args(norm_kind, max_norm, out, scratch, scratch_bytes, count))) return rc;
+  if ((rc = check_norm_args(norm_kind, max_norm, out, scratch, scratch_bytes, count, total))) return rc;
   if (reinterpret_cast<uintptr_t>(per_tensor) % 4) return fail(MUON_ERR_INVALID_ARG, "per_tensor is misaligned");
   std::vector<GradItem> it((size_t)count);
   for (int i = 0; i < count; ++i) {
@@ -1541,7 +1543,7 @@ int muon_clip_grads(muon_handle* h, const void* const* src, void* const* dst, co
   if ((rc = check_list(numels, src_dtypes, count, "src", &total))) return rc;
   if ((rc = check_list(numels, dst_dtypes, count, "dst", &total))) return rc;
   if (count > 0 && (!src || !dst)) return fail(MUON_ERR_INVALID_ARG, "src and dst are required");
-  if ((rc = check_norm_args(norm_kind, max_norm, out, scratch, scratch_bytes, count))) return rc;
+  if ((rc = check_norm_args(norm_kind, max_norm, out, scratch, scratch_bytes, count, total))) return rc;
   std::vector<GradItem> it((size_t)count);
   for (int i = 0; i < count; ++i) {
     const bool skip = src[i] == nullptr || numels[i] == 0;
@@ -1569,7 +1571,7 @@ int muon_clip_grads(muon_handle* h, const void* const* src, void* const* dst, co
   prof_call_begin(h);
   int launches = 0;
   double* partials = static_cast<double*>(scratch);
-  if (grad_is_small(it, total)) {
+  if (grad_is_small((int)it.size(), total)) {
     rc = enqueue_grad_small(h, it, norm_kind, true, max_norm, out, nullptr, st, &launches);
     h->last_launches = launches;
     return rc;

@@ -97,6 +97,7 @@ struct Lists {
   Column col[kMost];
   std::vector<int64_t> numel;
   int n = 0;
+  int64_t total = 0;
   bool same_ = false;
   const Column& second() const { return col[same_ ? 0 : 1]; }
   ~Lists() {
@@ -125,7 +126,7 @@ struct Lists {
       if (o == Py_None) continue;
       Row row;
       if (!take(o, device, allowed[0], true, row, col[0], (size_t)i, known)) return false;
-      numel[i] = THPVariable_Unpack(o).numel();
+      total += numel[i] = THPVariable_Unpack(o).numel();
       for (int k = 1; k < count; ++k)
         if (!take(PySequence_Fast_GET_ITEM(seq[k], i), device, allowed[k], false, row, col[k], (size_t)i, known))
           return false;
@@ -155,16 +156,18 @@ muon_handle* handle_of(PyObject* o) { return static_cast<muon_handle*>(PyLong_As
 
 // Results and scratch, from the memory of the stream that the call runs on.
 struct Buffers {
+  at::AutoDispatchBelowADInplaceOrView guard;   // plain tensors: nothing to record
   at::Tensor out, per, scratch;
-  size_t bytes;
-  Buffers(int64_t device, int n, bool per_tensor) {
-    at::AutoDispatchBelowADInplaceOrView guard;   // plain tensors: nothing to record
+  size_t bytes = 0;
+  Buffers(int64_t device, const Lists& l, bool per_tensor) {
     const auto on = at::TensorOptions().device(at::kCUDA, (c10::DeviceIndex)device);
-    bytes = MUON_GRAD_SCRATCH_BYTES(n);
     out = at::empty({2}, on.dtype(at::kFloat));
-    if (per_tensor) per = at::empty({n}, on.dtype(at::kFloat));
+    if (per_tensor) per = at::empty({l.n}, on.dtype(at::kFloat));
+    if (l.n <= MUON_GRAD_SMALL_COUNT && l.total <= MUON_GRAD_SMALL_NUMEL) return;
+    bytes = MUON_GRAD_SCRATCH_BYTES(l.n);
     scratch = at::empty({(int64_t)(bytes / 8)}, on.dtype(at::kDouble));
   }
+  void* scratch_ptr() { return bytes ? scratch.data_ptr() : nullptr; }
 };
 
 // bind(norm, clip, adamw): addresses of the C functions.
@@ -191,9 +194,9 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     Lists l;
     const int allowed[1] = {kAny};
     if (!l.read(&a[2], allowed, 1, device)) Py_RETURN_NONE;
-    Buffers b(device, l.n, per);
+    Buffers b(device, l, per);
     const int rc = c_norm(h, l.col[0].ptr.data(), l.numel.data(), l.col[0].type.data(), l.n, kind, max_norm,
-                          b.out.data_ptr<float>(), per ? b.per.data_ptr<float>() : nullptr, b.scratch.data_ptr(),
+                          b.out.data_ptr<float>(), per ? b.per.data_ptr<float>() : nullptr, b.scratch_ptr(),
                           b.bytes, c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
     if (rc) return PyLong_FromLong(rc);
     PyObject* r = PyTuple_New(per ? 3 : 2);
@@ -217,9 +220,9 @@ PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     Lists l;
     const int allowed[2] = {kAny, kAny};
     if (!l.read(&a[2], allowed, 2, device)) Py_RETURN_NONE;
-    Buffers b(device, l.n, false);
+    Buffers b(device, l, false);
     const int rc = c_clip(h, l.col[0].ptr.data(), l.second().ptr.data(), l.numel.data(), l.col[0].type.data(),
-                          l.second().type.data(), l.n, kind, max_norm, b.out.data_ptr<float>(), b.scratch.data_ptr(),
+                          l.second().type.data(), l.n, kind, max_norm, b.out.data_ptr<float>(), b.scratch_ptr(),
                           b.bytes, c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
     if (rc) return PyLong_FromLong(rc);
     return THPVariable_Wrap(b.out.select(0, 0));

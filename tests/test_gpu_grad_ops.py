@@ -347,6 +347,60 @@ def test_calls_on_two_streams_at_once(opt):
         assert all(abs(x.item() - want[k]) <= norm_tol(ts, 2.0) * want[k] for x in got[k])
 
 
+@pytest.mark.parametrize("sizes", [[3000, 17], [2_000_003, 17]])
+def test_calls_on_a_given_stream(opt, sizes):
+    p, g, m, v = adam_state(sizes, (BF16,), 55, 1)
+    old = [[t.clone() for t in ts] for ts in (p, m, v)]
+    before = [t.clone() for t in g]
+    out = [torch.empty_like(t) for t in g]
+    want, _ = exact_norm(g)
+    hyper = dict(lr=1e-3, step=4, betas=(0.9, 0.95), eps=1e-8, wd=0.1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    norm, scale, per = opt.grad_norm(g, max_norm=0.5 * want, per_tensor=True, stream=side)
+    opt.clip_grads(g, 0.5 * want, out=out, stream=side)
+    opt.adamw_step(p, out, m, v, stream=side, **hyper)
+    junk = [torch.full((70_000 + k,), 9.0, device=DEV) for k in range(50)]   # the current stream's memory moves on
+    torch.cuda.current_stream().wait_stream(side)
+    assert abs(norm.item() - want) <= norm_tol(g, 2.0) * want and per.numel() == len(g)
+    for i, b in enumerate(before):
+        assert_clipped(out[i], b, clip_of(want, 0.5 * want), norm_tol(g, 2.0) + U)
+        w, tol = adamw64(old[0][i], out[i], old[1][i], old[2][i], s=1.0, **hyper)
+        check_adamw((p[i], m[i], v[i]), w, tol)
+    assert all((j == 9).all() for j in junk)
+    assert abs(scale.item() - clip_of(want, 0.5 * want)) <= 7.0 * U
+
+
+def test_one_gradient_for_two_parameters(opt):
+    # Read twice, written never: allowed; it counts twice in the norm.
+    p, g, m, v = adam_state([900, 900], (F32,), 56)
+    g[1] = g[0]
+    old = [[t.clone() for t in ts] for ts in (p, m, v)]
+    norm, _ = opt.grad_norm(g)
+    assert abs(norm.item() - math.sqrt(2.0) * exact_norm(g[:1])[0]) <= 2 * U * norm.item()
+    opt.adamw_step(p, g, m, v, lr=1e-3, step=2)
+    for i in range(2):
+        w, tol = adamw64(old[0][i], g[0], old[1][i], old[2][i], 1e-3, 2, (0.9, 0.999), 1e-8, 0.1, 1.0)
+        check_adamw((p[i], m[i], v[i]), w, tol)
+
+
+def test_many_separate_tensors_in_any_order(opt):
+    # Addresses in no order: the overlap check sorts them.
+    sizes = np.random.default_rng(3).integers(1, 30_000, 300).tolist()
+    p, g, m, v = adam_state(sizes, (F32, F16), 57)
+    order = np.random.default_rng(4).permutation(len(sizes))
+    p, g, m, v = ([ts[i] for i in order] for ts in (p, g, m, v))
+    old = [[t.clone() for t in ts] for ts in (p, m, v)]
+    opt.adamw_step(p, g, m, v, lr=1e-3, step=2)
+    for i in range(0, len(p), 17):
+        w, tol = adamw64(old[0][i], g[i], old[1][i], old[2][i], 1e-3, 2, (0.9, 0.999), 1e-8, 0.1, 1.0)
+        check_adamw((p[i], m[i], v[i]), w, tol)
+    with pytest.raises(muon.MuonError):
+        opt.adamw_step(p + [p[150]], g + [g[150]], m + [m[150].clone()], v + [v[150].clone()], lr=1e-3, step=2)
+    with pytest.raises(muon.MuonError):
+        opt.clip_grads(g[:200] + [g[7][1:]], 1.0)
+
+
 def test_two_captured_graphs_replayed_in_turn(opt):
     lists = [tensors([70_001, 40], (F32,), seed=53), tensors([900, 123_457], (BF16,), seed=54)]
     graphs, outs = [], []

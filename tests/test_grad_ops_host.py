@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import muon_newton_schulz_03_b200 as muon
-from muon_newton_schulz_03_b200 import _bad_lists, _check_scalar, _dense, _grad_dtypes, _norm_kind
+from muon_newton_schulz_03_b200 import _bad_lists, _check_scalar, _dense, _grad_dtypes, _norm_kind, _sequence
 
 GRAD_SCRATCH_DOUBLES = 65536   # MUON_GRAD_SCRATCH_BYTES(count) = 8 * (65536 + count)
 BASE = 1 << 20      # made-up device addresses: nothing reads them
@@ -57,6 +57,7 @@ def _adamw(p=(BASE,), g=(BASE + 4096,), m=(BASE + 8192,), v=(BASE + 12288,), num
 
 @pytest.mark.parametrize("kw", [
     {}, {"kind": 1}, {"max_norm": math.inf}, {"max_norm": 0.0}, {"per": BASE}, {"ptrs": (None, BASE)},
+    {"scratch": None, "nbytes": 0}, {"numels": (131072, 0), "scratch": None, "nbytes": 0}, {"numels": (200_000, 1)},
     {"numels": (0, 0)}, {"ptrs": (), "numels": (), "dtypes": ()}, {"ptrs": (BASE, BASE)}, {"ptrs": (BASE + 4, BASE + 2)}])
 def test_norm_accepts(kw):
     assert _norm(**kw) == (1, "handle is NULL")
@@ -67,8 +68,9 @@ def test_norm_accepts(kw):
     ({"numels": (1 << 40, 1 << 40)}, "2^40"), ({"dtypes": (0, 3)}, "tensors[1]"), ({"dtypes": (-1, 0)}, "tensors[0]"),
     ({"ptrs": (BASE + 2, BASE)}, "tensors[0] is not aligned"), ({"ptrs": (BASE, BASE + 1)}, "tensors[1] is not aligned"),
     ({"kind": 2}, "norm_kind"), ({"max_norm": -1.0}, "max_norm"), ({"max_norm": math.nan}, "max_norm"),
-    ({"out": None}, "out"), ({"out": BASE + 2}, "out"), ({"per": BASE + 1}, "per_tensor"), ({"scratch": None}, "scratch"),
-    ({"scratch": BASE + 4}, "scratch"), ({"nbytes": 8 * GRAD_SCRATCH_DOUBLES}, "scratch holds")])
+    ({"out": None}, "out"), ({"out": BASE + 2}, "out"), ({"per": BASE + 1}, "per_tensor"), ({"numels": (131072, 1), "scratch": None}, "scratch"),
+    ({"numels": (200_000, 1), "scratch": BASE + 4}, "scratch"),
+    ({"numels": (200_000, 1), "nbytes": 8 * GRAD_SCRATCH_DOUBLES}, "scratch holds")])
 def test_norm_refuses(kw, msg):
     rc, text = _norm(**kw)
     assert rc == 1 and msg in text
@@ -200,3 +202,13 @@ def test_reader_refuses_bad_arguments():
     assert reader.adamw_step(0, 0, [], [], [], [], 1e-3, 0.9, 0.999, 1e-8, 0.0, torch.ones(1), None) is None
     with pytest.raises(TypeError):
         reader.clip_grads("handle", 0, [], [], 0, 1.0)
+
+
+def test_a_bare_tensor_is_not_a_list():
+    with pytest.raises(TypeError):
+        _sequence(torch.zeros(3, 4))
+    a = [torch.zeros(2)]
+    assert _sequence(a) is a and _sequence(iter(a)) == a
+    for bad in (1.0, torch.ones(2), torch.ones(1, dtype=torch.float64)):
+        with pytest.raises(ValueError):
+            _check_scalar(bad, "grad_scale", torch.float32, 0)
