@@ -4,13 +4,14 @@
 // own pass.
 //
 // All of them are bound by HBM (2 to 20 operations an element against 2 to
-// 32 bytes), so each makes one pass over its tensors in 16-byte accesses. A
+// 28 bytes), so each makes one pass over its tensors in 32-byte accesses. A
 // launch covers a whole list: a block works on one unit, 2^unit consecutive
-// elements of one tensor, and finds its tensor by binary search over the
-// units' prefix. The tables of pointers travel as kernel arguments (up to 32
-// KB), not through device memory: nothing is uploaded, a captured graph
-// holds its own copy, and calls on different streams share nothing. Longer
-// lists take several launches.
+// elements of one tensor, and finds its tensor through a short index. The
+// tables of pointers travel as kernel arguments (up to 32 KB), not through
+// device memory: nothing is uploaded, a captured graph holds its own copy,
+// and calls on different streams share nothing. Longer lists take several
+// launches. Measured rates: norm 7.2 to 7.3 TB/s, clipped copy and AdamW 7.0
+// (lists of 1 to 14 GB).
 //
 // Sums are held in fp64 and added in a fixed order (unit partials, then one
 // tree over them), so results repeat bit for bit.
@@ -29,7 +30,9 @@ constexpr int kFinishThreads = 1024;
 constexpr int kClusterBlocks = 8;   // the largest portable cluster
 
 // Waits for the kernel before this one on the stream (no effect in a normal
-// launch), and lets the next one be scheduled while this one drains.
+// launch); lets the next one be scheduled while this one drains. Kernels that
+// write tensors of the caller do not let it: what follows may be a kernel of
+// another library that reads weights before it waits.
 __device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dep_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -462,7 +465,6 @@ __global__ void __launch_bounds__(kThreads) g3_scale(const __grid_constant__ Sca
   const unsigned long long meta = t.meta[i];
   const UnitRange r = unit_range(meta, blk - t.units.unit0[i], unit);
   dep_wait();
-  dep_release();
   unit_scale<kThreads>(meta, t.src[i], t.dst[i], r, __ldcg(scale), threadIdx.x, once != 0);
 }
 
@@ -493,7 +495,7 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kSmallT
   const int nunits = t.units.unit0[t.units.count];
   cluster_arrive();   // every block of the cluster runs before another writes into it
   dep_wait();
-  dep_release();
+  if (!kScale) dep_release();
   bool started = false;
   for (int u = warp; u < nunits; u += kWarps) {
     const int i = find_tensor(t.units, u);
@@ -594,18 +596,15 @@ __global__ void __launch_bounds__(kThreads) g4_adamw(const __grid_constant__ Ada
   const UnitRange r = unit_range(meta, blk - t.units.unit0[i], unit);
   AdamW f{a.decay, a.b1, a.omb1, a.b2, a.omb2, a.eps, a.step_size, a.rsqrt_bc2, 1.0f};
   dep_wait();
-  dep_release();
   if (a.grad_scale != nullptr) f.gscale = __ldcg(a.grad_scale);
   if (a.step != nullptr) {
-    __shared__ float corr[2];
-    if (threadIdx.x == 0) {
-      const double k = (double)__ldcg(a.step);
-      corr[0] = (float)(a.lr / (1.0 - pow(a.beta1, k)));
-      corr[1] = (float)(1.0 / sqrt(1.0 - pow(a.beta2, k)));
-    }
-    __syncthreads();
-    f.step_size = corr[0];
-    f.rsqrt_bc2 = corr[1];
+    // 1 - beta^t = -expm1(t log beta), by every thread: t log beta is rounded
+    // once and expm1f is off by an ulp, so the corrections are off by 3 and
+    // 1.5 roundings, the factors made of them by 5 and 3.5. (One thread's pow
+    // in fp64 held its block up: 2.09 ms for 537 M elements, 2.01 without.)
+    const double t = (double)__ldcg(a.step);
+    f.step_size = a.lr / -expm1f((float)(t * a.log_beta1));
+    f.rsqrt_bc2 = 1.0f / sqrtf(-expm1f((float)(t * a.log_beta2)));
   }
   switch (grad_src(meta)) {
     case GRAD_F32: unit_adamw<GRAD_F32>(t.p[i], t.g[i], t.m[i], t.v[i], r, f, a.once != 0); break;

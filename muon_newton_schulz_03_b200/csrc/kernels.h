@@ -290,7 +290,8 @@ struct SpanTable {
 };
 
 struct AdamArgs {
-  double lr, beta1, beta2;          // for the step number on the device
+  double log_beta1, log_beta2;      // with lr, for a step number on the device
+  float lr;
   float decay, eps;                 // 1 - lr wd
   float b1, omb1, b2, omb2;         // beta1, 1 - beta1, ...
   float step_size, rsqrt_bc2;       // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t); unused with `step`

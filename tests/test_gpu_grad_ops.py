@@ -198,14 +198,16 @@ def test_permuted_and_shaped_tensors(opt, kind):
 
 # -- AdamW ------------------------------------------------------------------
 
-def adamw64(p, g, m, v, lr, step, betas, eps, wd, s):
+def adamw64(p, g, m, v, lr, step, betas, eps, wd, s, more=0):
     """The definition in 64 bits, and how far fp32 may be from it.
 
     m' = b1 m + (1 - b1) g: the constants, g's scaling, the product and the sum
     are 5 roundings of its two terms (which may cancel). v' has no cancelling
     terms: 7 roundings. The quotient's denominator: half of v's, the root, the
     correction, its product and eps: 7; the quotient, the step size and the
-    product with it: 3 more. p': the decay factor, its product, the sum."""
+    product with it: 3 more. p': the decay factor, its product, the sum.
+    A step number on the device: its factors are made in fp32, 4 roundings
+    more in the step size and 2.5 in the correction (``more`` = 6.5)."""
     b1, b2 = betas
     g = g.double() * s
     m1 = b1 * m.double() + (1 - b1) * g
@@ -218,7 +220,7 @@ def adamw64(p, g, m, v, lr, step, betas, eps, wd, s):
     tiny = torch.finfo(F32).tiny * torch.finfo(F32).eps
     tm = 5 * U * ((b1 * m.double()).abs() + ((1 - b1) * g).abs()) + tiny
     tv = 7 * U * v1 + tiny
-    tp = 2 * U * p64.abs() + lr1 * tm / den + 10 * U * d.abs() + U * p1.abs() + tiny
+    tp = 2 * U * p64.abs() + lr1 * tm / den + (10 + more) * U * d.abs() + U * p1.abs() + tiny
     # a v that fell below fp32's normal range moves the root by up to sqrt(tiny)
     tp = tp + torch.where(v1 < torch.finfo(F32).tiny, (d * math.sqrt(torch.finfo(F32).tiny) / den).abs(), 0.0 * d)
     return (p1, m1, v1), (tp, tm, tv)
@@ -454,9 +456,21 @@ def test_captured_training_tail(opt):
         norm = exact_norm(g)[0]
         assert abs(scale.item() - clip_of(norm, bound)) <= 7.0 * U * 1.001
         for i in range(len(p)):
-            want, tol = adamw64(old[0][i], g[i], old[1][i], old[2][i], step=t, s=scale.item(), **hyper)
+            want, tol = adamw64(old[0][i], g[i], old[1][i], old[2][i], step=t, s=scale.item(), more=6.5, **hyper)
             check_adamw((p[i], m[i], v[i]), want, tol)
     del graph, state
+
+
+@pytest.mark.parametrize("betas", [(0.9, 0.999), (0.0, 0.95), (0.95, 0.0), (0.999, 0.99999)])
+@pytest.mark.parametrize("step", [1, 2, 1000, 10 ** 9])
+def test_adamw_with_the_step_on_the_device(opt, betas, step):
+    p, g, m, v = adam_state([3001, 9], (F32, BF16), 61, 1, first=step == 1)
+    old = [[t.clone() for t in ts] for ts in (p, m, v)]
+    hyper = dict(lr=1e-3, betas=betas, eps=1e-8, wd=0.1)
+    opt.adamw_step(p, g, m, v, step=torch.tensor(step, device=DEV), **hyper)
+    for i in range(2):
+        w, tol = adamw64(old[0][i], g[i], old[1][i], old[2][i], step=step, s=1.0, more=6.5, **hyper)
+        check_adamw((p[i], m[i], v[i]), w, tol)
 
 
 def test_refusals_on_the_device(opt):
