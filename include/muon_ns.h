@@ -273,7 +273,7 @@ enum muon_norm_kind {
  * MUON_GRAD_SMALL_COUNT tensors and MUON_GRAD_SMALL_NUMEL elements (NULL ones
  * count too) takes one kernel and needs none. */
 #define MUON_GRAD_SCRATCH_BYTES(count) ((size_t)8 * ((size_t)65536 + (size_t)(count)))
-#define MUON_GRAD_SMALL_COUNT 256
+#define MUON_GRAD_SMALL_COUNT 512
 #define MUON_GRAD_SMALL_NUMEL 131072
 
 /* Norm of all tensors together and its clip multiplier.

@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads) g3_scale(const __grid_constant__ Sca
 // are level (3.6 against 2.9 us, 3.9 against 4.0): they overlap. At 2^18
 // elements the cluster's eight SMs are too few (5.3 us against 3.0).
 constexpr int kSmallThreads = 1024;
-constexpr int kSmallUnits = (int)(kGradSmallNumel >> kGradSmallUnit) + kGradCapMid;
+constexpr int kSmallUnits = (int)(kGradSmallNumel >> kGradSmallUnit) + kGradCapLarge;
 
 template <class Acc, int kCap, bool kScale>
 __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kSmallThreads)
@@ -646,10 +646,11 @@ void fill_index(UnitIndex<kCap>& x, int n, Units units) {
   x.shift = 0;
   if (total == 0) return;   // nothing will look anything up
   while ((total - 1) >> x.shift >= kBuckets) ++x.shift;
+  const int end = ((total - 1) >> x.shift) + 1;   // buckets in use
   int k = 0;
   for (int i = 0; i < n; ++i)
-    for (; k <= kBuckets && (long long)k << x.shift < x.unit0[i + 1]; ++k) x.tensor_of[k] = (unsigned short)i;
-  for (; k <= kBuckets; ++k) x.tensor_of[k] = (unsigned short)(n - 1);
+    for (; k < end && (long long)k << x.shift < x.unit0[i + 1]; ++k) x.tensor_of[k] = (unsigned short)i;
+  x.tensor_of[end] = (unsigned short)(n - 1);
 }
 
 template <int kCap>
@@ -726,6 +727,7 @@ template <class Acc>
 cudaError_t norm_for(const GradItem* it, int n, int unit, int keep, double* partials, cudaStream_t st, int* units) {
   if (n <= kGradCapSmall) return norm_launch<Acc, kGradCapSmall>(it, n, unit, keep, partials, st, units);
   if (n <= kGradCapMid) return norm_launch<Acc, kGradCapMid>(it, n, unit, keep, partials, st, units);
+  if (n <= kGradCapLarge) return norm_launch<Acc, kGradCapLarge>(it, n, unit, keep, partials, st, units);
   return norm_launch<Acc, kNormCap>(it, n, unit, keep, partials, st, units);
 }
 
@@ -735,6 +737,8 @@ cudaError_t finish_for(const GradItem* it, int n, int unit, const double* all, l
   if (!per_tensor) n = 0;
   if (n <= kGradCapSmall)
     return finish_launch<Acc, kGradCapSmall>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st);
+  if (n <= kGradCapLarge)
+    return finish_launch<Acc, kGradCapLarge>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st);
   return finish_launch<Acc, kNormCap>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st);
 }
 
@@ -742,7 +746,8 @@ template <class Acc>
 cudaError_t small_for(const GradItem* it, int n, bool scale, float max_norm, float* out,
                       float* per_tensor, cudaStream_t st) {
   if (n <= kGradCapSmall) return small_launch<Acc, kGradCapSmall>(it, n, scale, max_norm, out, per_tensor, st);
-  return small_launch<Acc, kGradCapMid>(it, n, scale, max_norm, out, per_tensor, st);
+  if (n <= kGradCapMid) return small_launch<Acc, kGradCapMid>(it, n, scale, max_norm, out, per_tensor, st);
+  return small_launch<Acc, kGradCapLarge>(it, n, scale, max_norm, out, per_tensor, st);
 }
 
 }  // namespace
@@ -771,12 +776,14 @@ cudaError_t launch_grad_scale(const GradItem* it, int n, int unit, int once, con
                               int* units) {
   if (n <= kGradCapSmall) return scale_launch<kGradCapSmall>(it, n, unit, once, scale, st, units);
   if (n <= kGradCapMid) return scale_launch<kGradCapMid>(it, n, unit, once, scale, st, units);
+  if (n <= kGradCapLarge) return scale_launch<kGradCapLarge>(it, n, unit, once, scale, st, units);
   return scale_launch<kScaleCap>(it, n, unit, once, scale, st, units);
 }
 
 cudaError_t launch_adamw(const AdamItem* it, int n, int unit, const AdamArgs& a, cudaStream_t st) {
   if (n <= kGradCapSmall) return adamw_launch<kGradCapSmall>(it, n, unit, a, st);
   if (n <= kGradCapMid) return adamw_launch<kGradCapMid>(it, n, unit, a, st);
+  if (n <= kGradCapLarge) return adamw_launch<kGradCapLarge>(it, n, unit, a, st);
   return adamw_launch<kAdamCap>(it, n, unit, a, st);
 }
 

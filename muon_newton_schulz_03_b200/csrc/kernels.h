@@ -207,6 +207,7 @@ inline void set_phases(AdamItem& x) {
 // the host 2.2 us more than 3 KB, 11 KB 1.1 us.
 constexpr int kGradCapSmall = 64;
 constexpr int kGradCapMid = 256;
+constexpr int kGradCapLarge = 512;
 constexpr int kNormCap = 1536;    // 20 bytes a tensor, and 0.5 KB of index
 constexpr int kScaleCap = 1088;   // 28
 constexpr int kAdamCap = 704;     // 44
@@ -312,7 +313,7 @@ cudaError_t launch_grad_finish(const GradItem* it, int n, int unit, int kind, co
                                float max_norm, float* out, const double* partials, float* per_tensor,
                                cudaStream_t st);
 // Both of the above, and with `scale` the clipped copy too, in one kernel:
-// lists of up to kGradCapMid tensors and kGradSmallNumel elements.
+// lists of up to kGradCapLarge tensors and kGradSmallNumel elements.
 cudaError_t launch_grad_small(const GradItem* it, int n, int kind, bool scale, float max_norm, float* out,
                               float* per_tensor, cudaStream_t st);
 // once: nothing of the list is read again soon.

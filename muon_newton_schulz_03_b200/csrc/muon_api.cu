@@ -1283,8 +1283,8 @@ int pick_unit(long long total, long long units, int least) {
 
 // Whether a list takes the one-kernel form.
 bool grad_is_small(int count, long long total) {
-  static_assert(MUON_GRAD_SMALL_COUNT == kGradCapMid && MUON_GRAD_SMALL_NUMEL == kGradSmallNumel, "small lists");
-  return count <= kGradCapMid && total <= kGradSmallNumel;
+  static_assert(MUON_GRAD_SMALL_COUNT == kGradCapLarge && MUON_GRAD_SMALL_NUMEL == kGradSmallNumel, "small lists");
+  return count <= kGradCapLarge && total <= kGradSmallNumel;
 }
 
 int enqueue_grad_small(muon_handle* h, const std::vector<GradItem>& it, int kind, bool scale, float max_norm,

@@ -114,7 +114,9 @@ class LayerwiseMuon:
     def step(self, params, grads, momenta, ns_steps: int = 5, **kw):
         """Update the matrices this rank owns, round by round, broadcasting
         each round's matrices from their owners while the next round runs.
-        Every rank must call this with the same shapes."""
+        Every rank must call this with the same shapes. ``kw``: as for
+        ``Muon.step``; a ``grad_scale`` is this rank's own tensor, made from
+        gradients that are the same on every rank."""
         shapes = [tuple(p.shape) for p in params]
         owners = self.owners(shapes, ns_steps)
         pending = []

@@ -127,7 +127,7 @@ def test_norm_of_nothing_and_skipped(opt):
     assert abs(per[2].item() - wb) <= U * 1.001 * wb
 
 
-@pytest.mark.parametrize("count", [64, 65, 704, 705, 1088, 1089, 1536, 1537, 3100])
+@pytest.mark.parametrize("count", [64, 65, 256, 257, 512, 513, 704, 705, 1088, 1089, 1536, 1537, 3100])
 def test_lists_longer_than_a_launch(opt, count):
     rng = np.random.default_rng(count)
     ts = tensors(rng.integers(0, 40, count).tolist(), (BF16, F32), seed=6, offset=1)
@@ -139,6 +139,25 @@ def test_lists_longer_than_a_launch(opt, count):
     opt.clip_grads(ts, 1.0)
     for t, b in zip(ts, before):
         assert_clipped(t, b, clip_of(want, 1.0), norm_tol(ts, 2.0) + U)
+
+
+@pytest.mark.parametrize("count,total", [(512, 131_072), (512, 131_073), (513, 131_072), (1, 131_072), (1, 131_073),
+                                         (256, 131_072), (257, 131_072)])
+@pytest.mark.parametrize("kind", [2.0, math.inf])
+def test_around_the_small_lists_limits(opt, count, total, kind):
+    # One kernel up to 512 tensors and 2^17 elements, several above; units of
+    # 1024 elements, one more per tensor at most.
+    sizes = [total // count] * (count - 1)
+    sizes.append(total - sum(sizes))
+    ts = tensors(sizes, (BF16, F32), seed=7, offset=3)
+    before = [t.clone() for t in ts]
+    norm, scale, per = opt.grad_norm(ts, max_norm=1.0, norm_type=kind, per_tensor=True)
+    want, want_per = exact_norm(ts, kind)
+    assert abs(norm.item() - want) <= norm_tol(ts, kind) * want
+    np.testing.assert_allclose(per.cpu().numpy(), want_per, rtol=norm_tol(ts, kind), atol=0)
+    opt.clip_grads(ts, 0.5 * want, norm_type=kind)
+    for t, b in zip(ts, before):
+        assert_clipped(t, b, clip_of(want, 0.5 * want), norm_tol(ts, kind) + U)
 
 
 @pytest.mark.parametrize("src", [F32, BF16, F16])
@@ -287,7 +306,7 @@ def test_adamw_leaves_everything_else(opt, gtype, offset):
     assert (keep == 3).all() and (k2 == 3).all() and (k3 == 3).all()
 
 
-@pytest.mark.parametrize("count", [64, 65, 705, 1500])
+@pytest.mark.parametrize("count", [64, 65, 257, 513, 705, 1500])
 def test_adamw_of_many(opt, count):
     rng = np.random.default_rng(count)
     sizes = rng.integers(0, 50, count).tolist()
@@ -532,6 +551,55 @@ def test_more_than_2_to_31_elements(opt, dtype):
         w, t = adamw64(p.new_ones(1), torch.tensor([g0], device=DEV), m.new_zeros(1), m.new_zeros(1), 1e-3, 1,
                        (0.9, 0.999), 1e-8, 0.0, 1.0)
         check_adamw((p[at:at + 1], m[at:at + 1], v[at:at + 1]), w, t)
+
+
+def test_a_module_s_parameters_and_gradients(opt):
+    # Parameters as a program has them, gradients from a backward pass, the
+    # tied one listed once; in and out of inference mode.
+    torch.manual_seed(0)
+    emb = torch.nn.Embedding(501, 48, device=DEV)
+    net = torch.nn.Sequential(torch.nn.Linear(48, 33, device=DEV), torch.nn.LayerNorm(33, device=DEV),
+                              torch.nn.Linear(33, 48, device=DEV))
+    ids = torch.randint(0, 400, (64,), device=DEV)          # rows above 400 get zero gradients
+    params = list(emb.parameters()) + list(net.parameters())
+    m, v = [torch.zeros_like(p) for p in params], [torch.zeros_like(p) for p in params]
+    for step in (1, 2):
+        for p in params:
+            p.grad = None
+        torch.nn.functional.linear(net(emb(ids)), emb.weight).square().mean().backward()
+        grads = [p.grad for p in params]
+        old = [[t.detach().clone() for t in ts] for ts in (params, m, v)]
+        want, _ = exact_norm(grads)
+        with torch.inference_mode(step == 2):
+            norm, scale = opt.grad_norm(grads, max_norm=0.5 * want)
+            opt.adamw_step(params, grads, m, v, lr=1e-3, step=step, grad_scale=scale)
+        assert abs(norm.item() - want) <= U * 1.001 * want
+        for i in range(len(params)):
+            w, tol = adamw64(old[0][i], grads[i], old[1][i], old[2][i], 1e-3, step, (0.9, 0.999), 1e-8, 0.1, scale.item())
+            check_adamw((params[i].detach(), m[i], v[i]), w, tol)
+    net(emb(ids)).sum().backward()                           # the next pass runs on the updated parameters
+
+
+def test_mostly_zero_gradients(opt):
+    # An embedding's: whole stretches of zeros, some signed, in 16 bits.
+    for dtype in (BF16, F16):
+        g = torch.zeros(300_000, dtype=dtype, device=DEV)
+        g[1::2] = -0.0
+        g[123_456] = 3.0
+        g[200_001] = -4.0
+        norm, _, per = opt.grad_norm([g, torch.zeros(5000, dtype=dtype, device=DEV)], per_tensor=True)
+        assert norm.item() == 5.0 and per.tolist() == [5.0, 0.0]
+        assert opt.grad_norm([g], norm_type=math.inf)[0].item() == 4.0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_subnormal_gradients(opt, dtype):
+    tiny = torch.finfo(dtype).tiny * torch.finfo(dtype).eps      # the smallest magnitude
+    g = torch.full((4099,), 3 * tiny, dtype=dtype, device=DEV)
+    want = exact_norm([g])[0]
+    tol = 5.0 * U * want + torch.finfo(F32).tiny * torch.finfo(F32).eps / 2   # and fp32's own last step
+    assert abs(opt.grad_norm([g])[0].item() - want) <= tol
+    assert opt.grad_norm([g], norm_type=math.inf)[0].item() == 3 * tiny
 
 
 # -- the multiplier in the Muon step -----------------------------------------
