@@ -251,11 +251,12 @@ int muon_step_scaled(muon_handle* h, float* const* params,
  *
  * Muon updates the 2D hidden matrices; embeddings, heads, norms and biases
  * go to AdamW ("Why Muon Works": hybrid routing), and clipping looks at all
- * of them together. The calls below take lists of tensors of any shape: tensor i is
- * numels[i] (>= 0) consecutive elements of type dtypes[i], aligned to its
- * element size (not to 16 bytes); 2^40 elements at most in all. count may be 0. The arrays are
- * host arrays, read during the call only. No device memory is allocated and
- * nothing is uploaded or kept between calls: the pointer tables travel as kernel arguments and all
+ * of them together. The calls below take lists of tensors of any shape:
+ * tensor i is numels[i] (>= 0) consecutive elements of type dtypes[i],
+ * aligned to its element size (not to 16 bytes); 2^40 elements at most in
+ * all. count may be 0. The arrays are host arrays, read during the call
+ * only. No device memory is allocated and nothing is uploaded or kept
+ * between calls: the pointer tables travel as kernel arguments and all
  * scratch is the caller's, so calls on several streams are independent and
  * every call may be captured in a CUDA graph. Sums are added in a fixed
  * order: results repeat bit for bit. */
