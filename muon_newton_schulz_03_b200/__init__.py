@@ -67,10 +67,11 @@ def _coeffs(coeffs):
     return c
 
 
-def _stream_handle(stream):
+def _stream_handle(stream, device):
+    """The given stream's handle; by default that of the device's current stream, whichever device is current."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -322,7 +323,11 @@ def plan_groups(shapes, cap_bytes: int, ns_precision: str = "bf16", small_path: 
 
 
 class Muon:
-    """A handle of the Muon library on one CUDA device."""
+    """A handle of the Muon library on one CUDA device.
+
+    Every call runs on ``stream``, by default the current one of the handle's
+    device (also while another device is current).
+    """
 
     def __init__(self, device: int = 0, scale_mode: str = "moonlight", extra_scale: float = 1.0,
                  ns_precision: str = "bf16", check_nonfinite: bool = False, num_sms: int = 0,
@@ -403,10 +408,10 @@ class Muon:
             check(self._lib.muon_step_scaled(self._h, pa, ga, ma, sa, n, float(lr), float(beta), int(bool(nesterov)),
                                              float(wd), int(ns_steps), _coeffs(coeffs), 1,
                                              _check_scalar(grad_scale, "grad_scale", torch.float32, self.device),
-                                             _stream_handle(stream)))
+                                             _stream_handle(stream, self.device)))
             return
         check(self._lib.muon_step(self._h, pa, ga, ma, sa, n, float(lr), float(beta), int(bool(nesterov)),
-                                  float(wd), int(ns_steps), _coeffs(coeffs), _stream_handle(stream)))
+                                  float(wd), int(ns_steps), _coeffs(coeffs), _stream_handle(stream, self.device)))
 
     def step_schedule(self, params, grads, momenta, coeff_table, lr, beta=0.95, nesterov=True, wd=0.1,
                       stream=None, grad_scale=None):
@@ -420,7 +425,7 @@ class Muon:
         check(self._lib.muon_step_scaled(self._h, pa, ga, ma, sa, n, float(lr), float(beta), int(bool(nesterov)),
                                          float(wd), len(rows), table, len(rows),
                                          _check_scalar(grad_scale, "grad_scale", torch.float32, self.device),
-                                         _stream_handle(stream)))
+                                         _stream_handle(stream, self.device)))
 
     # -- gradients of the whole model, and the tensors Muon does not take ----
     @functools.cached_property
@@ -444,8 +449,7 @@ class Muon:
         norm of each tensor (0 for a ``None``). Nothing waits for the GPU;
         pass ``scale`` on as ``grad_scale``. A NaN or infinity among the
         entries makes the norm NaN or infinite, the multiplier NaN or 0. The
-        call runs on ``stream`` (default: the handle's device's current one);
-        its results belong to that stream.
+        results belong to the call's stream.
         """
         if stream is not None:
             with self._on(stream):
@@ -521,7 +525,7 @@ class Muon:
             shapes.append((w.shape[0], w.shape[1], int(hr)))
         check(self._lib.muon_qk_clip(self._h, _ptr_array([w.data_ptr() for w in weights]), _shapes_array(shapes),
                                      _ptr_array([s.data_ptr() for s in s_max]), len(weights), float(tau),
-                                     _stream_handle(stream)))
+                                     _stream_handle(stream, self.device)))
 
     def step_host(self, params, grads, momenta, lr, beta=0.95, nesterov=True, wd=0.1, ns_steps=5,
                   coeffs=None, stream=None):
@@ -532,7 +536,7 @@ class Muon:
         """
         pa, ga, ma, sa, n = _marshal_step(params, grads, momenta, host=True)
         check(self._lib.muon_step_host(self._h, pa, ga, ma, sa, n, float(lr), float(beta), int(bool(nesterov)),
-                                       float(wd), int(ns_steps), _coeffs(coeffs), _stream_handle(stream)))
+                                       float(wd), int(ns_steps), _coeffs(coeffs), _stream_handle(stream, self.device)))
 
     # -- stages -------------------------------------------------------------
     def momentum_norm(self, grads, momenta, ys, sumsq, beta=0.95, nesterov=True, stream=None):
@@ -554,7 +558,7 @@ class Muon:
                                            _ptr_array([m.data_ptr() for m in momenta]),
                                            _ptr_array([y.data_ptr() for y in ys]), sumsq.data_ptr(),
                                            _shapes_array(shapes), len(shapes), float(beta), int(bool(nesterov)),
-                                           _stream_handle(stream)))
+                                           _stream_handle(stream, self.device)))
 
     def newton_schulz(self, x_in, x_out, shapes, sumsq=None, ns_steps=5, coeffs=None, stream=None):
         """Stage 2 on X-layout buffers; shapes is a list of (m, n)."""
@@ -567,7 +571,8 @@ class Muon:
         check(self._lib.muon_newton_schulz(self._h, _ptr_array([x.data_ptr() for x in x_in]),
                                            _ptr_array([x.data_ptr() for x in x_out]),
                                            None if sumsq is None else sumsq.data_ptr(), _shapes_array(sh),
-                                           len(sh), int(ns_steps), _coeffs(coeffs), _stream_handle(stream)))
+                                           len(sh), int(ns_steps), _coeffs(coeffs),
+                                           _stream_handle(stream, self.device)))
 
     def apply(self, params, os_, lr, wd, sumsq=None, stream=None):
         """Stage 3: params <- params (1 - lr wd) - lr scale o_scale O."""
@@ -584,7 +589,7 @@ class Muon:
         check(self._lib.muon_apply(self._h, _ptr_array([p.data_ptr() for p in params]),
                                    _ptr_array([_ptr(o) for o in os_]),
                                    None if sumsq is None else sumsq.data_ptr(), _shapes_array(shapes),
-                                   len(shapes), float(lr), float(wd), _stream_handle(stream)))
+                                   len(shapes), float(lr), float(wd), _stream_handle(stream, self.device)))
 
     def _check_on_device(self, t, what):
         if t.device.type != "cuda" or t.device.index != self.device:
@@ -609,7 +614,8 @@ class Muon:
         """(code, error_word, nonfinite_count); waits for the stream."""
         ew = ctypes.c_int32()
         nf = ctypes.c_uint64()
-        code = self._lib.muon_get_status(self._h, _stream_handle(stream), ctypes.byref(ew), ctypes.byref(nf))
+        code = self._lib.muon_get_status(self._h, _stream_handle(stream, self.device), ctypes.byref(ew),
+                                         ctypes.byref(nf))
         return code, ew.value, nf.value
 
     def workspace(self):
