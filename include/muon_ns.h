@@ -282,8 +282,9 @@ enum muon_norm_kind {
  *   norm_kind  : enum muon_norm_kind.
  *   max_norm   : >= 0; +infinity for no bound.
  *   out        : device float[2]: the norm, and min(1, max_norm / (norm +
- *                1e-6)); 1 without a bound. A NaN or infinite entry makes the
- *                norm NaN or infinite, and the multiplier NaN or 0.
+ *                1e-6)), made in fp64 from the norm before its rounding; 1
+ *                without a bound. A NaN or infinite entry makes the norm NaN
+ *                or infinite, and the multiplier NaN or 0.
  *   per_tensor : device float[count] or NULL: every tensor's norm (0 for a
  *                skipped one).
  *   scratch    : device memory, 8-byte aligned, scratch_bytes >=
@@ -291,7 +292,7 @@ enum muon_norm_kind {
  *                free for other use once the stream has passed the call. */
 int muon_grad_norm(muon_handle* h, const void* const* tensors,
                    const int64_t* numels, const int32_t* dtypes, int count,
-                   int norm_kind, float max_norm, float* out,
+                   int norm_kind, double max_norm, float* out,
                    float* per_tensor, void* scratch, size_t scratch_bytes,
                    void* stream);
 
@@ -303,7 +304,7 @@ int muon_grad_norm(muon_handle* h, const void* const* tensors,
 int muon_clip_grads(muon_handle* h, const void* const* src, void* const* dst,
                     const int64_t* numels, const int32_t* src_dtypes,
                     const int32_t* dst_dtypes, int count, int norm_kind,
-                    float max_norm, float* out, void* scratch,
+                    double max_norm, float* out, void* scratch,
                     size_t scratch_bytes, void* stream);
 
 /* One AdamW step, in place, on fp32 params and moments:

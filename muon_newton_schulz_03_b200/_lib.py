@@ -53,10 +53,10 @@ _SIGNATURES = {
                                    c_float, c_float, c_int, c_float, c_int, P(c_float), c_int, c_void_p]),
     "muon_step_scaled": (c_int, [c_void_p, P(c_void_p), P(c_void_p), P(c_void_p), P(ctypes.c_int32), c_int,
                                  c_float, c_float, c_int, c_float, c_int, P(c_float), c_int, c_void_p, c_void_p]),
-    "muon_grad_norm": (c_int, [c_void_p, P(c_void_p), P(ctypes.c_int64), P(ctypes.c_int32), c_int, c_int, c_float,
+    "muon_grad_norm": (c_int, [c_void_p, P(c_void_p), P(ctypes.c_int64), P(ctypes.c_int32), c_int, c_int, c_double,
                                c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "muon_clip_grads": (c_int, [c_void_p, P(c_void_p), P(c_void_p), P(ctypes.c_int64), P(ctypes.c_int32),
-                                P(ctypes.c_int32), c_int, c_int, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+                                P(ctypes.c_int32), c_int, c_int, c_double, c_void_p, c_void_p, c_size_t, c_void_p]),
     "muon_adamw_step": (c_int, [c_void_p, P(c_void_p), P(c_void_p), P(c_void_p), P(c_void_p), P(ctypes.c_int64),
                                 P(ctypes.c_int32), c_int, c_double, c_double, c_double, c_double, c_double,
                                 ctypes.c_int64, c_void_p, c_void_p, c_void_p]),

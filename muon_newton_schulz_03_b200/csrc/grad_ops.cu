@@ -334,9 +334,9 @@ __global__ void __launch_bounds__(kThreads, 8) g1_norm(const __grid_constant__ G
 }
 
 // min(1, max_norm / (norm + 1e-6)); NaN stays NaN, no bound is 1.
-__device__ __forceinline__ float clip_scale(double norm, float max_norm) {
+__device__ __forceinline__ float clip_scale(double norm, double max_norm) {
   if (isinf(max_norm)) return 1.0f;
-  const double c = (double)max_norm / (norm + 1e-6);
+  const double c = max_norm / (norm + 1e-6);
   return c >= 1.0 ? 1.0f : (float)c;
 }
 
@@ -369,7 +369,7 @@ __device__ __forceinline__ void tensor_norm(const int* unit0, int i, const Acc* 
 // one block 8 us, a cluster of eight 2.
 template <class Acc, int kCap>
 __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kFinishThreads)
-    g2_finish(const __grid_constant__ SpanTable<kCap> t, const Acc* all, long long nunits, float max_norm,
+    g2_finish(const __grid_constant__ SpanTable<kCap> t, const Acc* all, long long nunits, double max_norm,
               float* __restrict__ out, const Acc* partials, float* __restrict__ per_tensor) {
   __shared__ Acc sums[kClusterBlocks];
   dep_wait();
@@ -485,7 +485,7 @@ constexpr int kSmallUnits = (int)(kGradSmallNumel >> kGradSmallUnit) + kGradCapL
 
 template <class Acc, int kCap, bool kScale>
 __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kSmallThreads)
-    g5_small(const __grid_constant__ ScaleTable<kCap> t, float max_norm, float* __restrict__ out,
+    g5_small(const __grid_constant__ ScaleTable<kCap> t, double max_norm, float* __restrict__ out,
              float* __restrict__ per_tensor) {
   __shared__ Acc partials[kSmallUnits];
   __shared__ float shared_scale;
@@ -678,7 +678,7 @@ cudaError_t norm_launch(const GradItem* it, int n, int unit, int keep, double* p
 }
 
 template <class Acc, int kCap>
-cudaError_t finish_launch(const GradItem* it, int n, int unit, const double* all, long long nunits, float max_norm,
+cudaError_t finish_launch(const GradItem* it, int n, int unit, const double* all, long long nunits, double max_norm,
                           float* out, const double* partials, float* per_tensor, cudaStream_t st) {
   SpanTable<kCap> t;
   t.count = n;
@@ -701,7 +701,7 @@ cudaError_t scale_launch(const GradItem* it, int n, int unit, int once, const fl
 }
 
 template <class Acc, int kCap>
-cudaError_t small_launch(const GradItem* it, int n, bool scale, float max_norm, float* out,
+cudaError_t small_launch(const GradItem* it, int n, bool scale, double max_norm, float* out,
                          float* per_tensor, cudaStream_t st) {
   ScaleTable<kCap> t;
   fill(t, it, n, kGradSmallUnit);
@@ -732,7 +732,7 @@ cudaError_t norm_for(const GradItem* it, int n, int unit, int keep, double* part
 }
 
 template <class Acc>
-cudaError_t finish_for(const GradItem* it, int n, int unit, const double* all, long long nunits, float max_norm,
+cudaError_t finish_for(const GradItem* it, int n, int unit, const double* all, long long nunits, double max_norm,
                        float* out, const double* partials, float* per_tensor, cudaStream_t st) {
   if (!per_tensor) n = 0;
   if (n <= kGradCapSmall)
@@ -743,7 +743,7 @@ cudaError_t finish_for(const GradItem* it, int n, int unit, const double* all, l
 }
 
 template <class Acc>
-cudaError_t small_for(const GradItem* it, int n, bool scale, float max_norm, float* out,
+cudaError_t small_for(const GradItem* it, int n, bool scale, double max_norm, float* out,
                       float* per_tensor, cudaStream_t st) {
   if (n <= kGradCapSmall) return small_launch<Acc, kGradCapSmall>(it, n, scale, max_norm, out, per_tensor, st);
   if (n <= kGradCapMid) return small_launch<Acc, kGradCapMid>(it, n, scale, max_norm, out, per_tensor, st);
@@ -759,14 +759,14 @@ cudaError_t launch_grad_norm(const GradItem* it, int n, int unit, int keep, int 
 }
 
 cudaError_t launch_grad_finish(const GradItem* it, int n, int unit, int kind, const double* all, long long nunits,
-                               float max_norm, float* out, const double* partials, float* per_tensor,
+                               double max_norm, float* out, const double* partials, float* per_tensor,
                                cudaStream_t st) {
   return kind == GRAD_NORM_INF
              ? finish_for<MaxAbs>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st)
              : finish_for<SumSq>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st);
 }
 
-cudaError_t launch_grad_small(const GradItem* it, int n, int kind, bool scale, float max_norm,
+cudaError_t launch_grad_small(const GradItem* it, int n, int kind, bool scale, double max_norm,
                               float* out, float* per_tensor, cudaStream_t st) {
   return kind == GRAD_NORM_INF ? small_for<MaxAbs>(it, n, scale, max_norm, out, per_tensor, st)
                                : small_for<SumSq>(it, n, scale, max_norm, out, per_tensor, st);

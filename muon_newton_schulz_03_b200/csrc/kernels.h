@@ -310,11 +310,11 @@ cudaError_t launch_grad_norm(const GradItem* it, int n, int unit, int keep, int 
 // out (or NULL): norm and clip multiplier over all `nunits` partials at `all`.
 // per_tensor (or NULL): norms of these n tensors, whose partials start at `partials`.
 cudaError_t launch_grad_finish(const GradItem* it, int n, int unit, int kind, const double* all, long long nunits,
-                               float max_norm, float* out, const double* partials, float* per_tensor,
+                               double max_norm, float* out, const double* partials, float* per_tensor,
                                cudaStream_t st);
 // Both of the above, and with `scale` the clipped copy too, in one kernel:
 // lists of up to kGradCapLarge tensors and kGradSmallNumel elements.
-cudaError_t launch_grad_small(const GradItem* it, int n, int kind, bool scale, float max_norm, float* out,
+cudaError_t launch_grad_small(const GradItem* it, int n, int kind, bool scale, double max_norm, float* out,
                               float* per_tensor, cudaStream_t st);
 // once: nothing of the list is read again soon.
 cudaError_t launch_grad_scale(const GradItem* it, int n, int unit, int once, const float* scale, cudaStream_t st,

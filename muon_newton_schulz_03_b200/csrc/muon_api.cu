@@ -1287,7 +1287,7 @@ bool grad_is_small(int count, long long total) {
   return count <= kGradCapLarge && total <= kGradSmallNumel;
 }
 
-int enqueue_grad_small(muon_handle* h, const std::vector<GradItem>& it, int kind, bool scale, float max_norm,
+int enqueue_grad_small(muon_handle* h, const std::vector<GradItem>& it, int kind, bool scale, double max_norm,
                        float* out, float* per_tensor, cudaStream_t st, int* launches) {
   const int slot = prof_before(h, MUON_KERNEL_GRAD_SMALL, st);
   MUON_CUDA_TRY(launch_grad_small(it.data(), (int)it.size(), kind, scale, max_norm, out, per_tensor, st));
@@ -1298,7 +1298,7 @@ int enqueue_grad_small(muon_handle* h, const std::vector<GradItem>& it, int kind
 
 // Norm of the list into out (norm, multiplier) and per_tensor; the caller has
 // checked everything.
-int enqueue_grad_norm(muon_handle* h, const std::vector<GradItem>& it, long long total, int kind, float max_norm,
+int enqueue_grad_norm(muon_handle* h, const std::vector<GradItem>& it, long long total, int kind, double max_norm,
                       float* out, float* per_tensor, double* partials, cudaStream_t st, int* launches) {
   if (grad_is_small((int)it.size(), total))
     return enqueue_grad_small(h, it, kind, false, max_norm, out, per_tensor, st, launches);
@@ -1336,10 +1336,10 @@ int enqueue_grad_norm(muon_handle* h, const std::vector<GradItem>& it, long long
   return MUON_OK;
 }
 
-int check_norm_args(int norm_kind, float max_norm, const float* out, const void* scratch, size_t scratch_bytes,
+int check_norm_args(int norm_kind, double max_norm, const float* out, const void* scratch, size_t scratch_bytes,
                     int count, long long total) {
   if (norm_kind != MUON_NORM_L2 && norm_kind != MUON_NORM_INF) return fail(MUON_ERR_INVALID_ARG, "unknown norm_kind");
-  if (!(max_norm >= 0.0f)) return fail(MUON_ERR_INVALID_ARG, "max_norm must be >= 0 (infinity: no bound)");
+  if (!(max_norm >= 0.0)) return fail(MUON_ERR_INVALID_ARG, "max_norm must be >= 0 (infinity: no bound)");
   if (!out || reinterpret_cast<uintptr_t>(out) % 4) return fail(MUON_ERR_INVALID_ARG, "out is NULL or misaligned");
   if (grad_is_small(count, total)) return MUON_OK;
   if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 8)
@@ -1515,7 +1515,7 @@ int muon_qk_clip(muon_handle* h, float* const* weights, const int32_t* shapes, c
 }
 
 int muon_grad_norm(muon_handle* h, const void* const* tensors, const int64_t* numels, const int32_t* dtypes, int count,
-                   int norm_kind, float max_norm, float* out, float* per_tensor, void* scratch, size_t scratch_bytes,
+                   int norm_kind, double max_norm, float* out, float* per_tensor, void* scratch, size_t scratch_bytes,
                    void* stream) {
   return no_throw([&]() -> int {
     g_last_error.clear();
@@ -1547,7 +1547,7 @@ int muon_grad_norm(muon_handle* h, const void* const* tensors, const int64_t* nu
 }
 
 int muon_clip_grads(muon_handle* h, const void* const* src, void* const* dst, const int64_t* numels,
-                    const int32_t* src_dtypes, const int32_t* dst_dtypes, int count, int norm_kind, float max_norm,
+                    const int32_t* src_dtypes, const int32_t* dst_dtypes, int count, int norm_kind, double max_norm,
                     float* out, void* scratch, size_t scratch_bytes, void* stream) {
   return no_throw([&]() -> int {
     g_last_error.clear();

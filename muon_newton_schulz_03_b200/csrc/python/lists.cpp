@@ -188,7 +188,7 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     muon_handle* h = handle_of(a[0]);
     const int64_t device = PyLong_AsLongLong(a[1]);
     const int kind = (int)PyLong_AsLong(a[3]);
-    const float max_norm = (float)PyFloat_AsDouble(a[4]);
+    const double max_norm = PyFloat_AsDouble(a[4]);
     const bool per = PyObject_IsTrue(a[5]) == 1;
     if (PyErr_Occurred()) return nullptr;
     Lists l;
@@ -215,7 +215,7 @@ PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     muon_handle* h = handle_of(a[0]);
     const int64_t device = PyLong_AsLongLong(a[1]);
     const int kind = (int)PyLong_AsLong(a[4]);
-    const float max_norm = (float)PyFloat_AsDouble(a[5]);
+    const double max_norm = PyFloat_AsDouble(a[5]);
     if (PyErr_Occurred()) return nullptr;
     Lists l;
     const int allowed[2] = {kAny, kAny};
