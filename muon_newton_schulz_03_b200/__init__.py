@@ -326,7 +326,9 @@ class Muon:
     """A handle of the Muon library on one CUDA device.
 
     Every call runs on ``stream``, by default the current one of the handle's
-    device (also while another device is current).
+    device (also while another device is current). What ``clip_grads`` and
+    ``adamw_step`` write in place counts as modified to autograd (a captured
+    call: once, at its capture), as by torch's in-place operators.
     """
 
     def __init__(self, device: int = 0, scale_mode: str = "moonlight", extra_scale: float = 1.0,

@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
 #include <vector>
 
 #include "muon_ns.h"
@@ -29,10 +30,36 @@ constexpr int kAny = 7, kF32 = 1;   // allowed types, one bit each
 struct Column {
   std::vector<void*> ptr;
   std::vector<int32_t> type;
+  bool writes = false;                      // the call writes its tensors
+  std::vector<c10::TensorImpl*> versions;   // tensors whose version counters move then
   void resize(size_t n) {
     ptr.assign(n, nullptr);
     type.assign(n, 0);
+    if (writes) versions.reserve(n);
   }
+  // Moving a counter is an atomic (8 ns). Tensors cut from one buffer share
+  // theirs, and it is not moved again for a tensor whose counter is among the
+  // last four. Inference tensors have none.
+  void note(c10::TensorImpl* impl) {
+    uintptr_t id;   // which counter: the value of the one pointer that is kept of it, null without one
+    static_assert(sizeof(c10::VariableVersion) == sizeof(id), "a pointer to the counter");
+    std::memcpy(&id, &impl->version_counter(), sizeof(id));
+    if (id == 0 || id == recent[0] || id == recent[1] || id == recent[2] || id == recent[3]) return;
+    recent[at] = id;
+    at = (at + 1) % kRecent;
+    versions.push_back(impl);
+  }
+  // The call has written the tensors: a backward pass over a graph that saved
+  // the old values raises from now on.
+  void written() const {
+    for (c10::TensorImpl* impl : versions)
+      if (!impl->is_inference()) impl->bump_version();
+  }
+
+ private:
+  static constexpr int kRecent = 4;
+  uintptr_t recent[kRecent] = {};
+  int at = 0;
 };
 
 int type_of(const at::Tensor& t) {
@@ -68,7 +95,7 @@ bool take(PyObject* o, c10::Device device, int allowed, bool first, Row& row, Co
   if (!THPVariable_Check(o)) return false;
   const at::Tensor& t = THPVariable_Unpack(o);
   if (!is_plain(t, known)) return false;
-  const c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+  c10::TensorImpl* impl = t.unsafeGetTensorImpl();
   if (impl->device() != device) return false;
   const int type = type_of(t);
   if (type < 0 || !((allowed >> type) & 1)) return false;
@@ -84,6 +111,7 @@ bool take(PyObject* o, c10::Device device, int allowed, bool first, Row& row, Co
   const c10::Storage& storage = impl->unsafe_storage();
   char* base = storage ? static_cast<char*>(storage.unsafeGetStorageImpl()->mutable_data()) : nullptr;
   c.type[i] = type;
+  if (c.writes) c.note(impl);
   if (impl->numel() == 0) return true;
   if (base == nullptr) return false;
   c.ptr[i] = base + impl->storage_offset() * (type == MUON_DTYPE_F32 ? 4 : 2);
@@ -103,10 +131,12 @@ struct Lists {
   ~Lists() {
     for (PyObject* s : seq) Py_XDECREF(s);
   }
-  bool read(PyObject* const* lists, const int* allowed, int count, int64_t device_index) {
+  // `allowed` has every list's types; the lists from `first_written` on are written.
+  bool read(PyObject* const* lists, const int* allowed, int count, int first_written, int64_t device_index) {
     const c10::Device device(at::kCUDA, (c10::DeviceIndex)device_index);
     same_ = count == 2 && lists[0] == lists[1];   // clipped in place
-    if (same_) count = 1;
+    if (same_) count = 1, first_written = 0;
+    for (int k = first_written; k < count; ++k) col[k].writes = true;
     for (int k = 0; k < count; ++k) {
       seq[k] = PySequence_Fast(lists[k], "a list of tensors is needed");
       if (!seq[k]) {
@@ -193,7 +223,7 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (PyErr_Occurred()) return nullptr;
     Lists l;
     const int allowed[1] = {kAny};
-    if (!l.read(&a[2], allowed, 1, device)) Py_RETURN_NONE;
+    if (!l.read(&a[2], allowed, 1, 1, device)) Py_RETURN_NONE;
     Buffers b(device, l, per);
     const int rc = c_norm(h, l.col[0].ptr.data(), l.numel.data(), l.col[0].type.data(), l.n, kind, max_norm,
                           b.out.data_ptr<float>(), per ? b.per.data_ptr<float>() : nullptr, b.scratch_ptr(),
@@ -219,12 +249,13 @@ PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (PyErr_Occurred()) return nullptr;
     Lists l;
     const int allowed[2] = {kAny, kAny};
-    if (!l.read(&a[2], allowed, 2, device)) Py_RETURN_NONE;
+    if (!l.read(&a[2], allowed, 2, 1, device)) Py_RETURN_NONE;
     Buffers b(device, l, false);
     const int rc = c_clip(h, l.col[0].ptr.data(), l.second().ptr.data(), l.numel.data(), l.col[0].type.data(),
                           l.second().type.data(), l.n, kind, max_norm, b.out.data_ptr<float>(), b.scratch_ptr(),
                           b.bytes, c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
     if (rc) return PyLong_FromLong(rc);
+    l.second().written();
     return THPVariable_Wrap(b.out.select(0, 0));
   });
 }
@@ -259,12 +290,14 @@ PyObject* py_adamw(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (a[12] != Py_None && !one_element(a[12], device, at::kFloat, &scale)) Py_RETURN_NONE;
     Lists l;
     const int allowed[4] = {kAny, kF32, kF32, kF32};
-    if (!l.read(&a[2], allowed, 4, device)) Py_RETURN_NONE;
+    if (!l.read(&a[2], allowed, 4, 1, device)) Py_RETURN_NONE;
     const auto f = [&](int k) { return reinterpret_cast<float* const*>(l.col[k].ptr.data()); };
     const int rc = c_adamw(h, f(1), l.col[0].ptr.data(), f(2), f(3), l.numel.data(), l.col[0].type.data(), l.n, x[0],
                            x[1], x[2], x[3], x[4], step, static_cast<const int64_t*>(step_dev),
                            static_cast<const float*>(scale),
                            c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
+    if (!rc)
+      for (int k = 1; k < 4; ++k) l.col[k].written();
     return PyLong_FromLong(rc);
   });
 }
