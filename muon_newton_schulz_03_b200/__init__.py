@@ -75,6 +75,14 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _written(*lists, where=None):
+    """A call has written these tensors in place: their version counters move, so that a backward pass over a graph
+    that saved the old values raises. ``where``: only the entries whose partner there is not None."""
+    from torch.autograd.graph import increment_version
+    for ts in lists:
+        increment_version(list(ts) if where is None else [t for t, w in zip(ts, where) if w is not None])
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -326,9 +334,9 @@ class Muon:
     """A handle of the Muon library on one CUDA device.
 
     Every call runs on ``stream``, by default the current one of the handle's
-    device (also while another device is current). What ``clip_grads`` and
-    ``adamw_step`` write in place counts as modified to autograd (a captured
-    call: once, at its capture), as by torch's in-place operators.
+    device (also while another device is current). What a call writes
+    in place counts as modified to autograd (a captured call: once, at its
+    capture), as by torch's in-place operators.
     """
 
     def __init__(self, device: int = 0, scale_mode: str = "moonlight", extra_scale: float = 1.0,
@@ -404,6 +412,7 @@ class Muon:
         """
         if row_splits is not None:
             params, grads, momenta = split_rows(params, grads, momenta, row_splits)
+        params, grads, momenta = list(params), list(grads), list(momenta)
         pa, ga, ma, sa, n = _marshal_step(params, grads, momenta, device_index=self.device)
         if grad_scale is not None:
             import torch
@@ -411,9 +420,10 @@ class Muon:
                                              float(wd), int(ns_steps), _coeffs(coeffs), 1,
                                              _check_scalar(grad_scale, "grad_scale", torch.float32, self.device),
                                              _stream_handle(stream, self.device)))
-            return
-        check(self._lib.muon_step(self._h, pa, ga, ma, sa, n, float(lr), float(beta), int(bool(nesterov)),
-                                  float(wd), int(ns_steps), _coeffs(coeffs), _stream_handle(stream, self.device)))
+        else:
+            check(self._lib.muon_step(self._h, pa, ga, ma, sa, n, float(lr), float(beta), int(bool(nesterov)),
+                                      float(wd), int(ns_steps), _coeffs(coeffs), _stream_handle(stream, self.device)))
+        _written(params, momenta, where=grads)
 
     def step_schedule(self, params, grads, momenta, coeff_table, lr, beta=0.95, nesterov=True, wd=0.1,
                       stream=None, grad_scale=None):
@@ -423,11 +433,13 @@ class Muon:
         if not rows or any(len(r) != 3 for r in rows):
             raise ValueError("coeff_table must be a non-empty list of (a, b, c)")
         table = (ctypes.c_float * (3 * len(rows)))(*[v for r in rows for v in r])
+        params, grads, momenta = list(params), list(grads), list(momenta)
         pa, ga, ma, sa, n = _marshal_step(params, grads, momenta, device_index=self.device)
         check(self._lib.muon_step_scaled(self._h, pa, ga, ma, sa, n, float(lr), float(beta), int(bool(nesterov)),
                                          float(wd), len(rows), table, len(rows),
                                          _check_scalar(grad_scale, "grad_scale", torch.float32, self.device),
                                          _stream_handle(stream, self.device)))
+        _written(params, momenta, where=grads)
 
     # -- gradients of the whole model, and the tensors Muon does not take ----
     @functools.cached_property
@@ -528,6 +540,7 @@ class Muon:
         check(self._lib.muon_qk_clip(self._h, _ptr_array([w.data_ptr() for w in weights]), _shapes_array(shapes),
                                      _ptr_array([s.data_ptr() for s in s_max]), len(weights), float(tau),
                                      _stream_handle(stream, self.device)))
+        _written(weights)
 
     def step_host(self, params, grads, momenta, lr, beta=0.95, nesterov=True, wd=0.1, ns_steps=5,
                   coeffs=None, stream=None):
@@ -536,9 +549,11 @@ class Muon:
         The copies and the kernels are enqueued on ``stream``; synchronise it
         before reading params / momenta.
         """
+        params, grads, momenta = list(params), list(grads), list(momenta)
         pa, ga, ma, sa, n = _marshal_step(params, grads, momenta, host=True)
         check(self._lib.muon_step_host(self._h, pa, ga, ma, sa, n, float(lr), float(beta), int(bool(nesterov)),
                                        float(wd), int(ns_steps), _coeffs(coeffs), _stream_handle(stream, self.device)))
+        _written(params, momenta, where=grads)
 
     # -- stages -------------------------------------------------------------
     def momentum_norm(self, grads, momenta, ys, sumsq, beta=0.95, nesterov=True, stream=None):
@@ -561,6 +576,8 @@ class Muon:
                                            _ptr_array([y.data_ptr() for y in ys]), sumsq.data_ptr(),
                                            _shapes_array(shapes), len(shapes), float(beta), int(bool(nesterov)),
                                            _stream_handle(stream, self.device)))
+        _written(momenta, ys, where=grads)
+        _written([sumsq])
 
     def newton_schulz(self, x_in, x_out, shapes, sumsq=None, ns_steps=5, coeffs=None, stream=None):
         """Stage 2 on X-layout buffers; shapes is a list of (m, n)."""
@@ -575,6 +592,7 @@ class Muon:
                                            None if sumsq is None else sumsq.data_ptr(), _shapes_array(sh),
                                            len(sh), int(ns_steps), _coeffs(coeffs),
                                            _stream_handle(stream, self.device)))
+        _written(x_out)
 
     def apply(self, params, os_, lr, wd, sumsq=None, stream=None):
         """Stage 3: params <- params (1 - lr wd) - lr scale o_scale O."""
@@ -592,6 +610,7 @@ class Muon:
                                    _ptr_array([_ptr(o) for o in os_]),
                                    None if sumsq is None else sumsq.data_ptr(), _shapes_array(shapes),
                                    len(shapes), float(lr), float(wd), _stream_handle(stream, self.device)))
+        _written(params, where=os_)
 
     def _check_on_device(self, t, what):
         if t.device.type != "cuda" or t.device.index != self.device:

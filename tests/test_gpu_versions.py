@@ -105,3 +105,34 @@ def test_tensors_that_share_a_counter(opt, buffers):
     before = w._version
     opt.clip_grads([w.detach(), torch.ones(5, device=DEV)], 0.1)
     assert w._version > before
+
+
+@pytest.mark.parametrize("call", ["step", "scaled", "schedule", "split"])
+def test_the_muon_step_moves_what_it_writes(opt, call):
+    P, G, M = ([torch.full((64, 96), 0.25, device=DEV) for _ in range(3)] for _ in range(3))
+    G[1] = None
+    before, gv = versions(P, M), G[0]._version
+    kw = {"scaled": {"grad_scale": torch.ones(1, device=DEV)}, "split": {"row_splits": [32, None, [16, 48]]}}.get(call, {})
+    if call == "schedule":
+        opt.step_schedule(P, G, M, [muon.DEFAULT_COEFFS] * 2, lr=1e-3)
+    else:
+        opt.step(P, G, M, lr=1e-3, **kw)
+    for old, new in zip(before, versions(P, M)):
+        assert new[0] > old[0] and new[2] > old[2] and new[1] == old[1]
+    assert G[0]._version == gv
+
+
+def test_stages_and_qk_clip_move_what_they_write(opt):
+    g, m, p, w = (torch.full((64, 96), 0.25, device=DEV) for _ in range(4))
+    y, x, s = (muon.x_layout(64, 96, torch.bfloat16, DEV), muon.x_layout(64, 96, torch.bfloat16, DEV),
+               torch.zeros(1, dtype=torch.float64, device=DEV))
+    old = versions([g, m, y, x, s, p, w])[0]
+    opt.momentum_norm([g], [m], [y], s)
+    opt.newton_schulz([y], [x], [(64, 96)], sumsq=s)
+    opt.apply([p], [x], 1e-3, 0.1)
+    opt.qk_clip([w], [torch.full((4,), 200.0, device=DEV)], 16)
+    new = versions([g, m, y, x, s, p, w])[0]
+    assert new[0] == old[0] and all(b > a for a, b in zip(old[1:], new[1:]))
+    opt.momentum_norm([None], [m], [y], s)
+    opt.apply([p], [None], 1e-3, 0.1)
+    assert m._version == new[1] and p._version == new[5]
