@@ -30,9 +30,10 @@ constexpr int kFinishThreads = 1024;
 constexpr int kClusterBlocks = 8;   // the largest portable cluster
 
 // Waits for the kernel before this one on the stream (no effect in a normal
-// launch); lets the next one be scheduled while this one drains. Kernels that
-// write tensors of the caller do not let it: what follows may be a kernel of
-// another library that reads weights before it waits.
+// launch); lets the next one be scheduled while this one drains. Only kernels
+// that another kernel of the same call follows let it. What follows a call's
+// last kernel may be one of another library that reads parameters (weights, a
+// multiplier) before it waits.
 __device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dep_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -370,10 +371,10 @@ __device__ __forceinline__ void tensor_norm(const int* unit0, int i, const Acc* 
 template <class Acc, int kCap>
 __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kFinishThreads)
     g2_finish(const __grid_constant__ SpanTable<kCap> t, const Acc* all, long long nunits, double max_norm,
-              float* __restrict__ out, const Acc* partials, float* __restrict__ per_tensor) {
+              float* __restrict__ out, const Acc* partials, float* __restrict__ per_tensor, int followed) {
   __shared__ Acc sums[kClusterBlocks];
   dep_wait();
-  dep_release();
+  if (followed) dep_release();
   if (blockIdx.x >= kClusterBlocks) {
     const int i = (int)(blockIdx.x - kClusterBlocks) * (kFinishThreads / 32) + (int)(threadIdx.x >> 5);
     if (i < t.count) tensor_norm(t.unit0, i, partials, per_tensor);
@@ -495,7 +496,6 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kSmallT
   const int nunits = t.units.unit0[t.units.count];
   cluster_arrive();   // every block of the cluster runs before another writes into it
   dep_wait();
-  if (!kScale) dep_release();
   bool started = false;
   for (int u = warp; u < nunits; u += kWarps) {
     const int i = find_tensor(t.units, u);
@@ -679,7 +679,7 @@ cudaError_t norm_launch(const GradItem* it, int n, int unit, int keep, double* p
 
 template <class Acc, int kCap>
 cudaError_t finish_launch(const GradItem* it, int n, int unit, const double* all, long long nunits, double max_norm,
-                          float* out, const double* partials, float* per_tensor, cudaStream_t st) {
+                          float* out, const double* partials, float* per_tensor, int followed, cudaStream_t st) {
   SpanTable<kCap> t;
   t.count = n;
   t.unit0[0] = 0;
@@ -687,7 +687,7 @@ cudaError_t finish_launch(const GradItem* it, int n, int unit, const double* all
   const int per_block = kFinishThreads / 32, per_cluster = per_block * kClusterBlocks;
   const unsigned grid = (unsigned)(kClusterBlocks * (1 + (n + per_cluster - 1) / per_cluster));
   return launch_dep(g2_finish<Acc, kCap>, grid, kFinishThreads, st, t, reinterpret_cast<const Acc*>(all), nunits,
-                    max_norm, out, reinterpret_cast<const Acc*>(partials), per_tensor);
+                    max_norm, out, reinterpret_cast<const Acc*>(partials), per_tensor, followed);
 }
 
 template <int kCap>
@@ -733,13 +733,12 @@ cudaError_t norm_for(const GradItem* it, int n, int unit, int keep, double* part
 
 template <class Acc>
 cudaError_t finish_for(const GradItem* it, int n, int unit, const double* all, long long nunits, double max_norm,
-                       float* out, const double* partials, float* per_tensor, cudaStream_t st) {
+                       float* out, const double* partials, float* per_tensor, int followed, cudaStream_t st) {
   if (!per_tensor) n = 0;
-  if (n <= kGradCapSmall)
-    return finish_launch<Acc, kGradCapSmall>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st);
-  if (n <= kGradCapLarge)
-    return finish_launch<Acc, kGradCapLarge>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st);
-  return finish_launch<Acc, kNormCap>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st);
+  const auto launch = n <= kGradCapSmall   ? finish_launch<Acc, kGradCapSmall>
+                      : n <= kGradCapLarge ? finish_launch<Acc, kGradCapLarge>
+                                           : finish_launch<Acc, kNormCap>;
+  return launch(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, followed, st);
 }
 
 template <class Acc>
@@ -760,10 +759,10 @@ cudaError_t launch_grad_norm(const GradItem* it, int n, int unit, int keep, int 
 
 cudaError_t launch_grad_finish(const GradItem* it, int n, int unit, int kind, const double* all, long long nunits,
                                double max_norm, float* out, const double* partials, float* per_tensor,
-                               cudaStream_t st) {
+                               bool followed, cudaStream_t st) {
   return kind == GRAD_NORM_INF
-             ? finish_for<MaxAbs>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st)
-             : finish_for<SumSq>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, st);
+             ? finish_for<MaxAbs>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, followed, st)
+             : finish_for<SumSq>(it, n, unit, all, nunits, max_norm, out, partials, per_tensor, followed, st);
 }
 
 cudaError_t launch_grad_small(const GradItem* it, int n, int kind, bool scale, double max_norm,

@@ -309,9 +309,10 @@ cudaError_t launch_grad_norm(const GradItem* it, int n, int unit, int keep, int 
                              cudaStream_t st, int* units);
 // out (or NULL): norm and clip multiplier over all `nunits` partials at `all`.
 // per_tensor (or NULL): norms of these n tensors, whose partials start at `partials`.
+// followed: another kernel of the same call comes next on the stream.
 cudaError_t launch_grad_finish(const GradItem* it, int n, int unit, int kind, const double* all, long long nunits,
                                double max_norm, float* out, const double* partials, float* per_tensor,
-                               cudaStream_t st);
+                               bool followed, cudaStream_t st);
 // Both of the above, and with `scale` the clipped copy too, in one kernel:
 // lists of up to kGradCapLarge tensors and kGradSmallNumel elements.
 cudaError_t launch_grad_small(const GradItem* it, int n, int kind, bool scale, double max_norm, float* out,

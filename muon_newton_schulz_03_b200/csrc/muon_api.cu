@@ -1297,9 +1297,10 @@ int enqueue_grad_small(muon_handle* h, const std::vector<GradItem>& it, int kind
 }
 
 // Norm of the list into out (norm, multiplier) and per_tensor; the caller has
-// checked everything.
+// checked everything. followed: the call launches more kernels after these.
 int enqueue_grad_norm(muon_handle* h, const std::vector<GradItem>& it, long long total, int kind, double max_norm,
-                      float* out, float* per_tensor, double* partials, cudaStream_t st, int* launches) {
+                      float* out, float* per_tensor, double* partials, bool followed, cudaStream_t st,
+                      int* launches) {
   if (grad_is_small((int)it.size(), total))
     return enqueue_grad_small(h, it, kind, false, max_norm, out, per_tensor, st, launches);
   // 16 KB for a block: 3.5 GB took 469 us (7.46 TB/s) in units of 16 to 64
@@ -1329,7 +1330,7 @@ int enqueue_grad_norm(muon_handle* h, const std::vector<GradItem>& it, long long
     const int slot = prof_before(h, MUON_KERNEL_GRAD_FINISH, st);
     MUON_CUDA_TRY(launch_grad_finish(it.data() + i0, n, unit, kind, partials, base.back(), max_norm,
                                      last ? out : nullptr, partials + base[k], per_tensor ? per_tensor + i0 : nullptr,
-                                     st));
+                                     followed || !last, st));
     prof_after(h, slot, st);
     ++*launches;
   }
@@ -1539,7 +1540,7 @@ int muon_grad_norm(muon_handle* h, const void* const* tensors, const int64_t* nu
     prof_call_begin(h);
     int launches = 0;
     if ((rc = enqueue_grad_norm(h, it, total, norm_kind, max_norm, out, per_tensor, static_cast<double*>(scratch),
-                                static_cast<cudaStream_t>(stream), &launches)))
+                                false, static_cast<cudaStream_t>(stream), &launches)))
       return rc;
     h->last_launches = launches;
     return MUON_OK;
@@ -1589,7 +1590,10 @@ int muon_clip_grads(muon_handle* h, const void* const* src, void* const* dst, co
       h->last_launches = launches;
       return rc;
     }
-    if ((rc = enqueue_grad_norm(h, it, total, norm_kind, max_norm, out, nullptr, partials, st, &launches))) return rc;
+    bool any = false;   // something to write, which launches g3_scale
+    for (const GradItem& x : it) any = any || x.numel > 0;
+    if ((rc = enqueue_grad_norm(h, it, total, norm_kind, max_norm, out, nullptr, partials, any, st, &launches)))
+      return rc;
     // 16 or 32 KB of a list for a block, whose threads first wait for the
     // multiplier: 872 M bf16 elements took 506 us, 600 in units of 8 KB.
     const int unit = pick_unit(total, 1 << 20, 13);
