@@ -13,6 +13,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <limits>
 #include <list>
 #include <memory>
 #include <string>
@@ -1662,7 +1663,8 @@ int muon_adamw_step(muon_handle* h, float* const* params, const void* const* gra
     a.log_beta1 = std::log(beta1);   // of 0: -infinity, and 1 - beta^t is 1
     a.log_beta2 = std::log(beta2);
     a.decay = (float)(1.0 - lr * wd);
-    a.eps = (float)eps;
+    // A positive eps stays positive: an entry that never had a gradient is then 0 / eps, not 0 / 0.
+    a.eps = eps > 0.0 ? std::max((float)eps, std::numeric_limits<float>::denorm_min()) : 0.0f;
     a.step = reinterpret_cast<const long long*>(step_dev);
     a.b1 = (float)beta1;
     a.omb1 = (float)(1.0 - beta1);

@@ -47,3 +47,22 @@ def test_the_multiplier_is_one_rounding_off(opt, n, bound):
     s = bound / (1.5 + 1e-6)
     got = opt.grad_norm([g], max_norm=bound)[1].item()
     assert abs(got - s) <= 1.0001 * U * s
+
+
+# -- a positive eps below fp32's range ---------------------------------------
+
+@pytest.mark.parametrize("step", [1, 1000, "device"])
+@pytest.mark.parametrize("eps", [1e-30, 1e-44, 1e-46, 1e-60, 5e-324])
+def test_entries_without_gradients_only_decay_whatever_eps(opt, eps, step):
+    # Rows of an embedding that no token named: 0 / (0 + eps) = 0 in the definition.
+    n, lr, wd = 3000, 1e-2, 0.1
+    p, g, m, v = (torch.zeros(n, device=DEV) for _ in range(4))
+    p += 0.75
+    g[1000] = 0.5
+    t = torch.tensor(1, device=DEV) if step == "device" else step
+    opt.adamw_step([p], [g], [m], [v], lr=lr, step=t, eps=eps, wd=wd)
+    rest = torch.arange(n, device=DEV) != 1000
+    want = 0.75 * (1 - lr * wd)
+    assert ((p[rest].double() - want).abs() <= 3 * U * want).all()       # the factor, the product, the sum
+    assert (m[rest] == 0).all() and (v[rest] == 0).all()
+    assert math.isfinite(p[1000].item()) and p[1000] != p[0]
