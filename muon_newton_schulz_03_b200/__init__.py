@@ -232,6 +232,9 @@ def _check_scalar(t, what, dtype, device):
         return None
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != 1:
         raise ValueError(f"{what} must be a {dtype} tensor of one element")
+    if t.layout != torch.strided or t.is_neg():
+        raise ValueError(f"{what} must be a tensor of one element, stored as it is, got layout {t.layout}, "
+                         f"negated: {t.is_neg()}")
     if t.device.type != "cuda" or t.device.index != device:
         raise ValueError(f"{what} must be on cuda:{device}, got {t.device}")
     return t.data_ptr()
