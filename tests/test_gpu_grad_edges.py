@@ -2,6 +2,9 @@
 against their definitions in 64 bits (tolerances: see test_gpu_grad_ops)."""
 
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -9,9 +12,11 @@ import torch
 import muon_newton_schulz_03_b200 as muon
 
 from gpu_helpers import DEV
-from test_gpu_grad_ops import U, exact_norm
+from test_gpu_grad_ops import BF16, F32, U, clip_of, exact_norm, norm_tol, tensors
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -66,3 +71,81 @@ def test_entries_without_gradients_only_decay_whatever_eps(opt, eps, step):
     assert ((p[rest].double() - want).abs() <= 3 * U * want).all()       # the factor, the product, the sum
     assert (m[rest] == 0).all() and (v[rest] == 0).all()
     assert math.isfinite(p[1000].item()) and p[1000] != p[0]
+
+
+# -- one tensor of many units among small ones --------------------------------
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind", [2.0, math.inf])
+def test_per_tensor_norms_of_a_table_and_vectors(opt, dtype, kind):
+    ts = tensors([700, 1, 90_000_001, 0, 5000, 33], (dtype,), seed=80, offset=1, scale=0.1)
+    norm, _, per = opt.grad_norm(ts, norm_type=kind, per_tensor=True)
+    want, want_per = exact_norm(ts, kind)
+    tol = norm_tol(ts, kind)
+    assert abs(norm.item() - want) <= tol * want
+    assert all(abs(x - w) <= tol * w for x, w in zip(per.tolist(), want_per))
+
+
+# -- captured calls between other streams' work --------------------------------
+
+@pytest.mark.parametrize("n", [1000, 300_001])
+def test_captured_after_a_join_of_two_streams(opt, n):
+    # The call's kernels follow two branches of the graph at once, and another branch follows them.
+    g = [torch.zeros(n, device=DEV) for _ in range(2)]
+    p, m, v = torch.zeros(n, device=DEV), torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
+    src = torch.zeros((), device=DEV)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        g[0].copy_(src.expand(n))
+        with torch.cuda.stream(side):
+            g[1].copy_((2 * src).expand(n))
+        main.wait_stream(side)
+        norm, scale = opt.grad_norm(g, max_norm=1.0)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            seen = norm + scale
+        opt.adamw_step([p], [g[0]], [m], [v], lr=1e-3, step=1, wd=0.0, grad_scale=scale)
+        main.wait_stream(side)
+    for x in (0.25, 3.0, 1.0):
+        src.fill_(x)
+        m.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = x * math.sqrt(5.0 * n)
+        s = clip_of(want, 1.0)
+        assert abs(norm.item() - want) <= 1.001 * U * want and abs(scale.item() - s) <= 1.001 * U * s
+        assert seen.item() == (norm + scale).item()
+        first = 0.1 * s * x                                    # m' = (1 - beta1) s g
+        assert ((m.double() - first).abs() <= 5 * U * first).all()
+    del graph
+
+
+FIRST = """
+import math, torch
+import muon_newton_schulz_03_b200 as muon
+o = muon.Muon(device=0)
+n = {n}
+t = [torch.full((n,), 0.5, device="cuda") for _ in range(4)]
+one = torch.ones(1, dtype=torch.int64, device="cuda")
+graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph, stream=stream):
+    norm, scale = o.grad_norm(t, max_norm=1.0)
+    o.clip_grads(t[:1], 0.25)
+    o.adamw_step(t[1:2], t[:1], t[2:3], t[3:], lr=1e-3, step=one, grad_scale=scale)
+graph.replay()
+torch.cuda.synchronize()
+assert abs(norm.item() - math.sqrt(n)) <= 1e-6 * math.sqrt(n), norm.item()
+assert (t[1] != 0.5).all()
+del graph
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("n", [1000, 300_001])
+def test_the_first_calls_of_a_process_are_captured(n):
+    r = subprocess.run([sys.executable, "-c", FIRST.format(n=n)], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]

@@ -119,6 +119,8 @@ def test_step_scaled_refuses_a_null_handle():
 
 # -- the binding: dtype, layout and shape are checked before the device, so
 #    tensors in host memory reach every check
+#    of the function that names the reason (the compiled reader refuses any host
+#    tensor at once; its own checks are tested on the device)
 
 def _marshal(ts, *more, device=0):
     """What the binding does with a list: the reader refuses it, then the reason is raised."""
