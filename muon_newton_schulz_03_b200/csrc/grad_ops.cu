@@ -13,8 +13,9 @@
 // launches. Measured rates: norm 7.2 to 7.3 TB/s, clipped copy and AdamW 7.0
 // (lists of 1 to 14 GB).
 //
-// Sums are held in fp64 and added in a fixed order (unit partials, then one
-// tree over them), so results repeat bit for bit.
+// Sums are held in fp64, but for sixteen squares of 16-bit values at a time,
+// which are added in fp32 first (see SumSq::Part). The order is fixed (unit
+// partials, then one tree over them), so results repeat bit for bit.
 #include <algorithm>
 #include <type_traits>
 
@@ -413,7 +414,7 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kFinish
 // Clipped copy
 // ---------------------------------------------------------------------------
 
-// dst = s * src over a unit, each element rounded once to dst's type.
+// dst = s * src over a unit: an fp32 product, rounded to dst's type.
 template <int kSrc, int kDst, int kStride>
 __device__ __forceinline__ void unit_scale(const void* src, void* dst, const UnitRange& u, float s, int tid,
                                            bool once) {
@@ -477,10 +478,11 @@ __global__ void __launch_bounds__(kThreads) g3_scale(const __grid_constant__ Sca
 // and its barrier takes the place of the second and third launch. A warp takes
 // a unit of 1024 elements and writes its partial into every block's shared
 // memory; after the barrier every block adds them all, in the same order, to
-// have the multiplier. A call of 25 tensors, 2^17 elements: 7.2 us against 9.5
-// (norm), 7.3 against 12.2 (clip). Replayed from a graph the three launches
-// are level (3.6 against 2.9 us, 3.9 against 4.0): they overlap. At 2^18
-// elements the cluster's eight SMs are too few (5.3 us against 3.0).
+// have the multiplier. A call of 25 fp32 tensors, 2^17 elements: 5.7 us against
+// 8.3 (norm), 6.1 against 10.5 (clip into other tensors). Replayed from a graph
+// the two or three launches are level (3.7 against 4.1 us, 6.1 against 5.8):
+// they overlap. At 2^18 elements the cluster's eight SMs are too few (norm: 5.3
+// us against 4.4).
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallUnits = (int)(kGradSmallNumel >> kGradSmallUnit) + kGradCapLarge;
 

@@ -252,8 +252,10 @@ __host__ __device__ inline UnitRange unit_range(unsigned long long meta, int k, 
 
 // Where every tensor's units begin, and where to look for a unit's tensor: the
 // units fall into at most kBuckets buckets of 2^shift, and tensor_of[k] holds
-// the first unit of bucket k. A block then finds its tensor in two or three
-// dependent reads of its arguments instead of a search over the whole list.
+// the first unit of bucket k. A block then finds its tensor among those of a
+// bucket instead of the whole list: mostly two or three dependent reads of its
+// arguments; log2 of the tensors in a bucket at most (about 10, where a large
+// table's units make the buckets so wide that one holds all the vectors).
 constexpr int kBuckets = 256;
 template <int kCap>
 struct UnitIndex {
