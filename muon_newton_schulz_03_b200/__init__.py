@@ -198,7 +198,8 @@ def _check_tensor(t, what, dtypes, device, like=None):
     if like is not None:
         if t.shape != like.shape:
             raise ValueError(f"{what} shape {tuple(t.shape)} != {tuple(like.shape)}")
-        if not (t.is_contiguous() and like.is_contiguous()) and t.stride() != like.stride():
+        if not (t.is_contiguous() and like.is_contiguous()) and any(
+                n != 1 and a != b for n, a, b in zip(t.shape, t.stride(), like.stride())):
             raise ValueError(f"{what} has strides {t.stride()}, its partner {like.stride()}")
     if t.device.type != "cuda" or t.device.index != device:
         raise ValueError(f"{what} must be on cuda:{device}, got {t.device}")

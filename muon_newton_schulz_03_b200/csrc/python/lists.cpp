@@ -88,6 +88,13 @@ struct Row {
   bool contiguous;
 };
 
+// Whether elements are at the same places: a dimension of one has any stride.
+bool same_places(const Row& row, c10::IntArrayRef strides) {
+  for (size_t d = 0; d < strides.size(); ++d)
+    if (row.sizes[d] != 1 && row.strides[d] != strides[d]) return false;
+  return true;
+}
+
 // A dense strided tensor of an allowed type on the device; `first`: of its
 // row, whose others are laid out like it.
 bool take(PyObject* o, c10::Device device, int allowed, bool first, Row& row, Column& c, size_t i,
@@ -105,7 +112,7 @@ bool take(PyObject* o, c10::Device device, int allowed, bool first, Row& row, Co
     row = Row{impl->sizes(), impl->strides(), contiguous};
   } else {
     if (impl->sizes() != row.sizes) return false;
-    if (!(contiguous && row.contiguous) && impl->strides() != row.strides) return false;
+    if (!(contiguous && row.contiguous) && !same_places(row, impl->strides())) return false;
   }
   // data_ptr(), without looking the element size up
   const c10::Storage& storage = impl->unsafe_storage();

@@ -118,3 +118,21 @@ def test_a_transposed_row_against_contiguous_ones(opt):
         with pytest.raises(ValueError) as e:
             opt.adamw_step(*([x] for x in row), lr=0.1, step=1)
         assert "strides" in str(e.value) and untouched(row)
+
+
+def test_one_layout_by_other_strides_is_taken(opt):
+    # A dimension of one element has any stride; the others say where the elements are.
+    def make(first):
+        t = full(15)
+        t[:] = torch.arange(15, device=DEV) / 8
+        return t.as_strided((1, 5, 3), (first, 1, 5))
+    g, out = [make(15)], [make(7)]
+    opt.clip_grads(g, 1.0, out=out)
+    whole = g[0].clone()
+    opt.clip_grads([whole], 1.0)
+    assert torch.equal(out[0], whole)
+    p, m, v = make(1), make(99), make(15)
+    q, n, w = p.clone(), m.clone(), v.clone()
+    opt.adamw_step([p], g, [m], [v], lr=0.1, step=2)
+    opt.adamw_step([q], [g[0].clone()], [n], [w], lr=0.1, step=2)
+    assert torch.equal(p, q) and torch.equal(m, n) and torch.equal(v, w)
